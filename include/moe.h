@@ -343,6 +343,124 @@ int moe_experts_batched_masked(const uint8_t* a_q, const float* a_s, const int32
                                const uint8_t* w2, const float* w2_s, uint16_t* out, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* ---- bf16 experts, forward and backward ------------------------------------
+ * The same layer on unquantised weights, with its gradients: permute of bf16
+ * rows -> grouped product (w13) -> SiLU-mul -> grouped product (w2) ->
+ * moe_unpermute_weight_reduce; backwards through the entry points below, and
+ * moe_unpermute_weight_reduce with apply_on_input = 1 as the permute's
+ * gradient (a token's gradient is the plain sum of its rows').  The valid
+ * rows of expert e are [expert_offsets[e], expert_offsets[e] + counts[e]),
+ * cut at expert_offsets[e+1] and at cap_rows, so inconsistent offsets or
+ * counts never move an access outside the buffers.  Rows that are not valid
+ * may hold anything (NaN too): they are never read into a result and never
+ * written.  Widths are positive multiples of 8 up to 65536 unless a
+ * declaration says otherwise.  Sums are fp32 and every bf16 output is rounded
+ * once.
+ *
+ * rows_hint (the products): about how many rows are valid in all, Mc * topk
+ * for instance; <= 0 means cap_rows.  It picks the tile shape, so it changes
+ * the speed, and the order of the fp32 sums with it, but any value is
+ * correct. */
+
+/* moe_permute for bf16 rows: x [Mc,K] bf16, a_perm [cap_rows,K] bf16;
+ * a_perm[row] = x[t] with the rows, counts, expert_offsets, inv_perm and
+ * row_src of moe_permute.  K: positive multiple of 128, at most 65536.  Other
+ * arguments, limits and errors as moe_permute. */
+int moe_permute_bf16(const uint16_t* x, const int32_t* topk_ids, int64_t Mc, int32_t K, int32_t topk,
+                     const int32_t* expert_map, int32_t Eg, int32_t El, int32_t align, int64_t cap_rows,
+                     uint16_t* a_perm, int32_t* counts, int32_t* expert_offsets, int32_t* inv_perm,
+                     int32_t* row_src, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Grouped product: for every valid row r of expert e and n < n_out
+ *   out[r,n] = bf16( sum_k a[r,k] * w[e,n,k] ).
+ * a [cap_rows,k_in], w [El,n_out,k_in], out [cap_rows,n_out], all bf16; out
+ * overlaps neither input. */
+int moe_grouped_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* expert_offsets,
+                          const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out, int32_t k_in,
+                          int64_t rows_hint, uint16_t* out, void* stream);
+
+/* Its gradient by the rows: for every valid row r of expert e and k < k_in
+ *   dx[r,k] = bf16( sum_n dy[r,n] * w[e,n,k] ).
+ * dy [cap_rows,n_out], w [El,n_out,k_in], dx [cap_rows,k_in], all bf16; dx
+ * overlaps neither input. */
+int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int32_t* expert_offsets,
+                                const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out,
+                                int32_t k_in, int64_t rows_hint, uint16_t* dx, void* stream);
+
+/* Its gradient by the weights, for every expert e, n < n_out and k < k_in
+ *   dw[e,n,k] = sum over e's valid rows r of dy[r,n] * a[r,k]
+ * (0 for an expert without rows), in fp32 or rounded once to bf16
+ * (dw_dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16).  accumulate = 1 (fp32 only)
+ * adds it to what dw holds.  dy [cap_rows,n_out], a [cap_rows,k_in] bf16,
+ * dw [El,n_out,k_in]; dw overlaps neither input. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* expert_offsets,
+                                const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out,
+                                int32_t k_in, int64_t rows_hint, int32_t dw_dtype, int32_t accumulate, void* dw,
+                                void* stream);
+
+/* SiLU-mul on bf16 rows h [rows,2n] (gate columns [0,n), up [n,2n)):
+ *   act[r,c] = bf16( g * u / (1 + exp(-g)) ),  g = h[r,c], u = h[r,n+c].
+ * act [rows,n].  expert_offsets / counts: NULL = every row valid; otherwise
+ * only valid rows are read and written.  act does not overlap h. */
+int moe_silu_mul(const uint16_t* h, int64_t rows, int32_t n, const int32_t* expert_offsets,
+                 const int32_t* counts, int32_t El, uint16_t* act, void* stream);
+
+/* Its gradient: with s = 1 / (1 + exp(-g)) and d = dact[r,c]
+ *   dh[r,c] = bf16( d * u * s * (1 + g * (1 - s)) ),
+ *   dh[r,n+c] = bf16( d * g * s ).
+ * dact [rows,n], dh [rows,2n]; dh may be h itself (in place) and overlaps
+ * nothing else.  Other arguments as moe_silu_mul. */
+int moe_silu_mul_bwd(const uint16_t* h, const uint16_t* dact, int64_t rows, int32_t n,
+                     const int32_t* expert_offsets, const int32_t* counts, int32_t El, uint16_t* dh,
+                     void* stream);
+
+/* Gradient of moe_unpermute_weight_reduce (apply_on_input = 0): for each
+ * token t and k with 0 <= row < y_rows, row = inv_perm[t,k],
+ *   dy[row,c] = bf16( topk_weights[t,k] * dout[t,c] ),
+ *   dweights[t,k] = sum_c y[row,c] * dout[t,c]  (fp32),
+ * and dweights[t,k] = 0 for the other pairs.  dout [Mc,K], y and dy
+ * [y_rows,K] bf16 (rows that no pair names are not written; a row named by
+ * two pairs receives either), inv_perm, topk_weights and dweights [Mc,topk].
+ * K: positive multiple of 128.  dy overlaps neither dout nor y. */
+int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows,
+                                    const int32_t* inv_perm, const float* topk_weights, int64_t Mc, int32_t K,
+                                    int32_t topk, uint16_t* dy, float* dweights, void* stream);
+
+/* Global gradient norm over many tensors, and clipping.  A tensor of the
+ * list: `grad` its values (contiguous, aligned to its element only), `out`
+ * where moe_grad_clip writes (grad itself, or memory that no other field of
+ * the list overlaps; moe_grad_sumsq does not read the field), numel values (0
+ * allowed), dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32 for both.  The list is host
+ * memory and is not needed after the call returns; it goes to the kernels by
+ * value, 64 tensors a launch. */
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t numel;
+    int32_t dtype;
+    int32_t reserved;   /* 0 */
+} moe_grad_tensor;
+
+/* Workspace bytes moe_grad_sumsq needs for a list of num_tensors. */
+int moe_grad_workspace_size(int32_t num_tensors, size_t* bytes);
+
+/* sumsq[0] = sum over all tensors and elements of g^2, in fp64 (squares and
+ * sums: no fp32 value overflows or vanishes), in an order fixed by the list,
+ * so equal calls give equal bits.  sumsq: device double, 16-byte aligned.
+ * Ranks that hold parts of the parameters all-reduce (sum) it before
+ * moe_grad_clip. */
+int moe_grad_sumsq(const moe_grad_tensor* tensors, int32_t num_tensors, double* sumsq, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* out = g * c in the tensor's dtype (one rounding), with norm = sqrt(sumsq[0])
+ * and c = min(1, max_norm / (norm + 1e-6)) (NaN where norm is NaN).  norm:
+ * device float [1], 16-byte aligned, receives the norm before clipping (or
+ * NULL).  max_norm >= 0.  An in-place tensor is not touched when c is 1. */
+int moe_grad_clip(const moe_grad_tensor* tensors, int32_t num_tensors, const double* sumsq, float max_norm,
+                  float* norm, void* stream);
+
 /* Plain HBM streams, timed beside the memory-bound kernels as their measured
  * ceilings (not part of the layer): MOE_STREAM_READ reads `bytes` from src
  * (dst: >= 16 bytes of device memory, receives nothing unless the data hash

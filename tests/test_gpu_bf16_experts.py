@@ -1,0 +1,593 @@
+"""The bf16 experts' operators on the GPU against plain 64-bit implementations.
+
+Tolerances, derived before the first run.  A sum of C products of bf16 values
+(each product exact in fp32) accumulated in fp32 in any order is off by at
+most C * 2^-23 * T, T the sum of the products' magnitudes (2^-24 a step for
+rounding to nearest, 2^-23 should the matrix unit truncate); rounding the
+result to bf16 adds 2^-8 relative (2^-24 for fp32).  Both bounds are added.
+"""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import unpermute_count_expert_amd as moe
+from tests.gpu_helpers import announce
+
+DEV = "cuda:0"
+BF, F32, F64, I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
+EPS = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+TINY = 2.0 ** -133   # half the smallest bf16 denormal's spacing
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def bf(shape, g, scale=1.0):
+    return (torch.randn(shape, generator=g) * scale).to(BF)
+
+
+def segments(counts, align, cap_extra=5):
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + -(-c // align) * align)
+    return off, off[-1] + cap_extra
+
+
+def valid_mask(counts, off, cap):
+    m = torch.zeros(cap, dtype=torch.bool)
+    for e, c in enumerate(counts):
+        m[off[e]:off[e] + c] = True
+    return m
+
+
+def poison(t, mask):
+    t = t.clone()
+    t[~mask] = float("nan")
+    return t
+
+
+def close(got, ref, mag, terms, what=""):
+    got = got.double().cpu()
+    tol = EPS[BF if what.endswith("bf16") else F32] * ref.abs() + terms * 2.0 ** -23 * mag + TINY
+    bad = ~((got - ref).abs() <= tol * (1 + 2.0 ** -7))
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off; worst " \
+                          f"{float(((got - ref).abs() / tol).nan_to_num(1e30).max()):.3g} tolerances"
+
+
+def i32(v):
+    return torch.tensor(v, dtype=I32, device=DEV)
+
+
+SENT = 0x7b7b   # a bf16 bit pattern that no result here has
+
+
+def sentinel(shape):
+    return torch.full(shape, SENT, dtype=torch.int16, device=DEV).view(BF)
+
+
+def untouched(t, mask):
+    return bool((t.cpu().view(torch.int16)[~mask] == SENT).all())
+
+
+COUNTS = {
+    "none": [0, 0, 0],
+    "one": [0, 1, 0, 0],
+    "few": [1, 0, 3, 16, 2, 0, 17],
+    "ragged": [63, 0, 65, 1, 130, 128, 15],
+    "long": [300, 0, 257, 7],
+    "single_expert": [200],
+}
+
+
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("n,k", [(8, 8), (64, 128), (40, 136), (264, 1000), (520, 72), (1000, 264)])
+@pytest.mark.parametrize("hint", [1, 0, 1 << 20])
+def test_products(counts, n, k, hint):
+    announce("products", counts, n, k, hint)
+    cs = COUNTS[counts]
+    E = len(cs)
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    g = gen(n * 7 + k + len(cs))
+    a, dy, w = bf((cap, k), g), bf((cap, n), g, 0.1), bf((E, n, k), g, 0.05)
+    A, D, W = (poison(a, mask).to(DEV), poison(dy, mask).to(DEV), w.to(DEV))
+    O, Cn = i32(off), i32(cs)
+    out, dx = sentinel((cap, n)), sentinel((cap, k))
+    dwf = torch.full((E, n, k), 3.25, device=DEV)
+    dwb = sentinel((E, n, k))
+    moe.moe_grouped_gemm_bf16(A, W, O, Cn, out, hint)
+    moe.moe_grouped_gemm_bf16_dgrad(D, W, O, Cn, dx, hint)
+    moe.moe_grouped_gemm_bf16_wgrad(D, A, O, Cn, dwf, 0, hint)
+    moe.moe_grouped_gemm_bf16_wgrad(D, A, O, Cn, dwb, 0, hint)
+    acc = torch.full((E, n, k), 3.25, device=DEV)
+    moe.moe_grouped_gemm_bf16_wgrad(D, A, O, Cn, acc, 1, hint)
+    torch.cuda.synchronize()
+    assert untouched(out, mask) and untouched(dx, mask)
+    for e, c in enumerate(cs):
+        r = slice(off[e], off[e] + c)
+        ae, de, we = a[r].double(), dy[r].double(), w[e].double()
+        close(out[r], ae @ we.T, ae.abs() @ we.abs().T, k, "out bf16")
+        close(dx[r], de @ we, de.abs() @ we.abs(), n, "dx bf16")
+        ref, mag = de.T @ ae, de.abs().T @ ae.abs()
+        close(dwf[e], ref, mag, c, "dw f32")
+        close(dwb[e], ref, mag, c, "dw bf16")
+        close(acc[e], ref + 3.25, mag + 3.25, c + 1, "dw accumulated f32")
+
+
+def run_products(a, dy, w, off, cs, hint=0):
+    cap, k = a.shape
+    E, n, _ = w.shape
+    O, Cn = i32(off), i32(cs)
+    out, dx = sentinel((cap, n)), sentinel((cap, k))
+    dw = torch.empty((E, n, k), device=DEV)
+    A, D, W = a.to(DEV), dy.to(DEV), w.to(DEV)
+    moe.moe_grouped_gemm_bf16(A, W, O, Cn, out, hint)
+    moe.moe_grouped_gemm_bf16_dgrad(D, W, O, Cn, dx, hint)
+    moe.moe_grouped_gemm_bf16_wgrad(D, A, O, Cn, dw, 0, hint)
+    torch.cuda.synchronize()
+    return out.cpu(), dx.cpu(), dw.cpu()
+
+
+def test_products_inconsistent_segments_are_cut():
+    """A count past its slot is cut at the next segment and at the buffer; a negative one is empty."""
+    off, cap = [0, 16, 32, 40], 44
+    g = gen(5)
+    a, dy, w = bf((cap, 64), g), bf((cap, 40), g), bf((3, 40, 64), g)
+    for hint in (1, 1 << 20):
+        got = run_products(a, dy, w, off, [100, -3, 900], hint)
+        want = run_products(a, dy, w, off, [16, 0, 8], hint)
+        for x, y in zip(got, want):
+            assert torch.equal(x.view(torch.int16 if x.dtype == BF else I32), y.view(torch.int16 if y.dtype == BF else I32))
+        # offsets past the buffer and out of order: in bounds, no valid row beyond the buffer
+        run_products(a, dy, w, [0, 500, 20, 44], [4, 9, 30], hint)
+        run_products(a, dy, w, [-7, 44, 44, 10], [50, 9, 30], hint)
+
+
+@pytest.mark.parametrize("hint", [1, 1 << 20])
+def test_products_non_finite_values_stay_in_their_rows(hint):
+    """Infinities and NaN of one expert's rows or weights reach only the outputs that contain them."""
+    cs, n, k = [20, 3, 40], 72, 104
+    off, cap = segments(cs, 16)
+    g = gen(6)
+    a, dy, w = bf((cap, k), g), bf((cap, n), g), bf((3, n, k), g)
+    base = run_products(a, dy, w, off, cs, hint)
+    a2, dy2 = a.clone(), dy.clone()
+    a2[off[1] + 1, 5] = float("inf")
+    dy2[off[1] + 2, 7] = float("nan")
+    out, dx, dw = run_products(a2, dy2, w, off, cs, hint)
+    rows = torch.ones(cap, dtype=torch.bool)
+    rows[off[1] + 1] = False
+    assert torch.equal(out.view(torch.int16)[rows], base[0].view(torch.int16)[rows])
+    assert not torch.isfinite(out[off[1] + 1].float()).any()
+    rows = torch.ones(cap, dtype=torch.bool)
+    rows[off[1] + 2] = False
+    assert torch.equal(dx.view(torch.int16)[rows], base[1].view(torch.int16)[rows])
+    assert torch.isnan(dx[off[1] + 2].float()).all()
+    assert torch.equal(dw[[0, 2]], base[2][[0, 2]])
+    ref = dy2[off[1]:off[1] + 3].double().T @ a2[off[1]:off[1] + 3].double()
+    assert torch.equal(torch.isfinite(dw[1]), torch.isfinite(ref))
+
+
+def test_products_many_experts():
+    """1024 experts, most without rows."""
+    g = gen(7)
+    cs = [0] * 1024
+    for e, c in ((0, 2), (1, 1), (511, 40), (777, 5), (1023, 3)):
+        cs[e] = c
+    off, cap = segments(cs, 16, 0)
+    a, dy, w = bf((cap, 32), g), bf((cap, 16), g), bf((1024, 16, 32), g)
+    for hint in (1, 1 << 24):
+        out, dx, dw = run_products(a, dy, w, off, cs, hint)
+        for e in (0, 1, 2, 511, 777, 1023):
+            r = slice(off[e], off[e] + cs[e])
+            ae, de, we = a[r].double(), dy[r].double(), w[e].double()
+            close(out[r], ae @ we.T, ae.abs() @ we.abs().T, 32, "out bf16")
+            close(dx[r], de @ we, de.abs() @ we.abs(), 16, "dx bf16")
+            close(dw[e], de.T @ ae, de.abs().T @ ae.abs(), cs[e], "dw f32")
+
+
+def test_products_match_differences():
+    """The products are linear: moving the rows (weights) by an exactly representable step moves <out, dy> by the
+    step's inner product with dx (dw), here in integers, where every rounding is exact."""
+    g = gen(8)
+    cs = [5, 0, 18]
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g).to(BF)
+    a, dy, w, da, dw_ = ints(cap, 24), ints(cap, 16), ints(3, 16, 24), ints(cap, 24), ints(3, 16, 24)
+    f = lambda aa, ww: (run_products(aa, dy, ww, off, cs)[0].double()[mask] * dy.double()[mask]).sum()
+    _, dx, dw = run_products(a, dy, w, off, cs)
+    assert f(a + da, w) - f(a - da, w) == 2 * (dx.double()[mask] * da.double()[mask]).sum()
+    assert f(a, w + dw_) - f(a, w - dw_) == 2 * (dw.double() * dw_.double()).sum()
+
+
+# ---- permute -----------------------------------------------------------------------
+@pytest.mark.parametrize("M,topk,Eg,El,align,K", [
+    (1, 1, 4, 4, 16, 128), (7, 3, 8, 8, 32, 256), (130, 8, 128, 64, 128, 384), (1500, 4, 60, 60, 16, 128),
+    (0, 2, 4, 4, 16, 128), (33, 2, 3000, 40, 64, 128)])
+def test_permute_rows(M, topk, Eg, El, align, K):
+    announce("permute_bf16", M, topk, Eg, El, align, K)
+    g = gen(M + K)
+    x = bf((M, K), g)
+    ids = torch.randint(-1, Eg, (M, topk), generator=g, dtype=torch.int64).to(I32)   # the same expert twice too
+    emap = None
+    if El < Eg:
+        emap = torch.full((Eg,), -1, dtype=I32)
+        emap[torch.randperm(Eg, generator=g)[:El]] = torch.arange(El, dtype=I32)
+    cap = moe.moe_max_rows(M, topk, El, align) + 3
+    a = sentinel((cap, K))
+    counts, off, inv = i32([9] * El), i32([9] * (El + 1)), torch.empty((M, topk), dtype=I32, device=DEV)
+    src = torch.empty((cap,), dtype=I32, device=DEV)
+    ws = torch.empty(moe.moe_permute_workspace_size(M, topk, El), dtype=torch.uint8, device=DEV)
+    moe.moe_permute_bf16(x.to(DEV), ids.to(DEV), None if emap is None else emap.to(DEV), Eg, El, align, cap, a,
+                         counts, off, inv, src, ws)
+    torch.cuda.synchronize()
+    loc = [[(-1 if i < 0 else i if emap is None else int(emap[i])) for i in row] for row in ids.tolist()]
+    want_c = [sum(l == e for row in loc for l in row) for e in range(El)]
+    want_o, _ = segments(want_c, align)
+    nxt, want_inv, want_src = list(want_o), [], [-1] * cap
+    for t, row in enumerate(loc):
+        for l in row:
+            want_inv.append(nxt[l] if l >= 0 else -1)
+            if l >= 0:
+                want_src[nxt[l]] = t
+                nxt[l] += 1
+    assert counts.tolist() == want_c and off.tolist() == want_o
+    assert inv.reshape(-1).tolist() == want_inv and src.tolist() == want_src
+    rows = torch.tensor([s >= 0 for s in want_src])
+    assert torch.equal(a.cpu()[rows], x[[s for s in want_src if s >= 0]])
+    assert untouched(a, rows)
+
+
+# ---- SiLU-mul ----------------------------------------------------------------------
+def silu_ref(h, d):
+    n = h.shape[1] // 2
+    g, u = h[:, :n].double(), h[:, n:].double()
+    s = 1 / (1 + torch.exp(-g))
+    return g * s * u, d * u * s * (1 + g * (1 - s)), d * g * s
+
+
+def test_silu_reference_matches_differences():
+    g = gen(3)
+    h = torch.randn(5, 12, generator=g, dtype=F64) * 3
+    d = torch.randn(5, 6, generator=g, dtype=F64)
+    _, dg, du = silu_ref(h, d)
+    step = 1e-6
+    for c in range(12):
+        hp, hm = h.clone(), h.clone()
+        hp[:, c] += step
+        hm[:, c] -= step
+        num = ((silu_ref(hp, d)[0] - silu_ref(hm, d)[0]) * d).sum(1) / (2 * step)
+        ref = dg[:, c] if c < 6 else du[:, c - 6]
+        assert torch.allclose(num, ref, rtol=1e-7, atol=1e-8)
+
+
+@pytest.mark.parametrize("counts,n", [("none", 8), ("one", 128), ("few", 40), ("ragged", 1000), ("long", 4096),
+                                      (None, 8), (None, 264)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_silu_mul(counts, n, in_place):
+    announce("silu", counts, n, in_place)
+    if counts is None:
+        cap, off, cs = 37, None, None
+        mask = torch.ones(cap, dtype=torch.bool)
+        args = ()
+    else:
+        cs = COUNTS[counts]
+        off, cap = segments(cs, 16)
+        mask = valid_mask(cs, off, cap)
+        args = (i32(off), i32(cs), len(cs))
+    g = gen(n)
+    h, d = bf((cap, 2 * n), g, 4.0), bf((cap, n), g)
+    H, D = poison(h, mask).to(DEV), poison(d, mask).to(DEV)
+    act = sentinel((cap, n))
+    moe.moe_silu_mul(H, n, act, *args)
+    if in_place:
+        H[~mask.to(DEV)] = sentinel((1, 1))
+        dh = H
+    else:
+        dh = sentinel((cap, 2 * n))
+    moe.moe_silu_mul_bwd(H, D, n, dh, *args)
+    torch.cuda.synchronize()
+    assert untouched(act, mask) and untouched(dh, mask)
+    ra, rg, ru = silu_ref(h[mask], d[mask].double())
+    # e^-g from the hardware exp2 of -g log2(e) rounded in fp32: at most 2^-22 (2 + |g|) relative; s inherits it,
+    # 1 - s is off by 2^-24 absolute on top of s's error, and each of at most five further operations adds 2^-24
+    gg = h[mask][:, :n].double()
+    rel = 2.0 ** -22 * (4 + gg.abs())
+    for got, ref, extra in ((act[mask], ra, 0), (dh[mask][:, n:], ru, 0),
+                            (dh[mask][:, :n], rg,
+                             (d[mask].double() * h[mask][:, n:].double()).abs() * (1 + gg.abs()) * rel)):
+        err = (got.double().cpu() - ref).abs()
+        tol = (2.0 ** -8 + rel) * ref.abs() + extra + TINY
+        assert (err <= tol * (1 + 2.0 ** -7)).all(), float((err / tol).max())
+
+
+def test_silu_mul_extremes():
+    """Large gates of either sign, zeros, infinities and NaN: as the formula in 64 bits says, where it has a value."""
+    gates = [0.0, -0.0, 1e-30, -1e-30, 20.0, -20.0, 87.0, -87.0, 300.0, -300.0, 1e30, -1e30, 3e38, -3e38,
+             float("inf"), float("nan")]
+    n = len(gates)
+    h = torch.tensor([gates + [1.5] * n]).to(BF)
+    d = torch.full((1, n), 0.5, dtype=BF)
+    act, dh = sentinel((1, n)), sentinel((1, 2 * n))
+    moe.moe_silu_mul(h.to(DEV), n, act)
+    moe.moe_silu_mul_bwd(h.to(DEV), d.to(DEV), n, dh)
+    act, dh = act.cpu().double()[0], dh.cpu().double()[0]
+    for i, g in enumerate(h[0, :n].double().tolist()):
+        if g != g:
+            assert act[i].isnan() and dh[i].isnan() and dh[n + i].isnan()
+            continue
+        s = 1 / (1 + np.exp(-g)) if g > -700 else 0.0
+        want = (g * s * 1.5, 0.5 * 1.5 * s * (1 + (g * (1 - s) if np.isfinite(g) else 0.0)), 0.5 * g * s)
+        for j, (got, ref) in enumerate(zip((act[i], dh[i], dh[n + i]), want)):
+            if g == float("inf") and j == 1:
+                continue   # inf * 0 in the formula
+            # past the largest bf16, (2 - 2^-7) 2^127, by half a step and more: infinity
+            ref = float("inf") if ref >= (2 - 2.0 ** -8) * 2.0 ** 127 else ref
+            # below 2^-126 the fp32 sigmoid may be flushed: |g| s is under 2^-118 there
+            assert abs(got - ref) <= 2.0 ** -7 * abs(ref) + 2.0 ** -118 or got == ref, (g, float(got), ref)
+
+
+# ---- weighted unpermute's gradient -----------------------------------------------------
+@pytest.mark.parametrize("M,topk,K,rows", [(1, 1, 128, 4), (5, 8, 640, 60), (130, 3, 2048, 500), (3000, 2, 128, 7000),
+                                           (2, 256, 256, 600), (4, 2, 128, 0)])
+def test_unpermute_bwd(M, topk, K, rows):
+    announce("unpermute_bwd", M, topk, K, rows)
+    g = gen(M + K)
+    y, dout = bf((rows, K), g), bf((M, K), g)
+    tw = torch.rand((M, topk), generator=g)
+    place = torch.randperm(max(rows, M * topk), generator=g)[:M * topk].reshape(M, topk).to(I32)   # some >= rows
+    place[torch.rand((M, topk), generator=g) < 0.3] = -1
+    place[-1] = -1   # a token with no row
+    dy = sentinel((rows, K))
+    dtw = torch.full((M, topk), 7.0, device=DEV)
+    moe.moe_unpermute_weight_reduce_bwd(dout.to(DEV), y.to(DEV), place.to(DEV), tw.to(DEV), dy, dtw)
+    torch.cuda.synchronize()
+    ok = (place >= 0) & (place < rows)
+    t, k = ok.nonzero(as_tuple=True)
+    r = place[t, k].long()
+    named = torch.zeros(rows, dtype=torch.bool)
+    named[r] = True
+    assert untouched(dy, named)
+    yd, dd = y[r].double(), dout[t].double()
+    close(dtw.cpu()[t, k], (yd * dd).sum(1), (yd * dd).abs().sum(1), K, "dweights f32")
+    assert (dtw.cpu()[~ok] == 0).all()
+    ref = tw[t, k, None].double() * dd
+    close(dy.cpu()[r], ref, ref.abs(), 1, "dy bf16")
+
+
+def test_unpermute_bwd_matches_differences():
+    """out is linear in y and in the weights: exact in small integers."""
+    g = gen(4)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g).float()
+    M, topk, K, rows = 6, 2, 128, 12
+    y, dout, tw = ints(rows, K).to(BF), ints(M, K).to(BF), ints(M, topk)
+    inv = torch.randperm(rows, generator=g).reshape(M, topk).to(I32)
+
+    def f(yy, ww):
+        out = torch.empty((M, K), dtype=BF, device=DEV)
+        moe.moe_unpermute_weight_reduce(yy.to(DEV), inv.to(DEV), ww.to(DEV), 0, out)
+        return (out.cpu().double() * dout.double()).sum()
+
+    dy, dtw = torch.empty((rows, K), dtype=BF, device=DEV), torch.empty((M, topk), device=DEV)
+    moe.moe_unpermute_weight_reduce_bwd(dout.to(DEV), y.to(DEV), inv.to(DEV), tw.to(DEV), dy, dtw)
+    sy, sw = ints(rows, K).to(BF), ints(M, topk)
+    assert f(y + sy, tw) - f(y - sy, tw) == 2 * (dy.cpu().double() * sy.double()).sum()
+    assert f(y, tw + sw) - f(y, tw - sw) == 2 * (dtw.cpu().double() * sw.double()).sum()
+
+
+# ---- global norm and clipping ------------------------------------------------------------
+def clip(grads, outs, max_norm):
+    s = torch.full((1,), -1.0, dtype=F64, device=DEV)
+    nrm = torch.full((1,), -1.0, device=DEV)
+    ws = torch.empty(moe.moe_grad_workspace_size(len(grads)), dtype=torch.uint8, device=DEV)
+    moe.moe_grad_sumsq(grads, s, ws)
+    moe.moe_grad_clip(grads, outs, s, max_norm, nrm)
+    torch.cuda.synchronize()
+    return float(s), float(nrm)
+
+
+def flat_views(sizes, skew, g, scale=1.0):
+    """Tensors end to end in one buffer a type, so most start off 16-byte alignment."""
+    out = []
+    for i, m in enumerate(sizes):
+        dt = BF if (i + skew) % 2 else F32
+        buf = (torch.randn(m + skew, generator=g) * scale).to(dt).to(DEV)
+        out.append(buf[skew:])
+    return out
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 3, 0], [7, 8, 9, 15, 16, 17], [4097, 1, 100000, 8191],
+                                   [5] * 200, [3_000_001, 17], []])
+@pytest.mark.parametrize("skew", [0, 1, 3])
+@pytest.mark.parametrize("max_norm", [0.0, 0.5, 1e9])
+def test_clip(sizes, skew, max_norm):
+    announce("clip", len(sizes), skew, max_norm)
+    grads = flat_views(sizes, skew, gen(len(sizes) + skew))
+    before = [t.cpu() for t in grads]
+    ref = sum(float((t.double() ** 2).sum()) for t in before)
+    for mode in ("same skew", "other skew", "in place"):
+        if mode == "in place":
+            outs = None
+        else:
+            sk = skew if mode == "same skew" else skew + 1
+            outs = [torch.full((t.numel() + sk + 9,), 5.0, dtype=t.dtype, device=DEV)[sk:sk + t.numel()] for t in grads]
+        s, nrm = clip(grads, outs, max_norm)
+        # fp64 sums of exact squares: n 2^-53 relative; the norm is rounded once to fp32
+        assert abs(s - ref) <= max(1, sum(sizes)) * 2.0 ** -52 * ref
+        assert abs(nrm - ref ** 0.5) <= 2.0 ** -24 * ref ** 0.5 * 1.01
+        c = min(1.0, max_norm / (ref ** 0.5 + 1e-6))
+        for i, t in enumerate(before):
+            got = (grads if outs is None else outs)[i].cpu().double()
+            want = t.double() * c
+            # c: the norm's rounding, the sum, the quotient and the product, 2^-24 each, then the rounding to t's type
+            tol = (4 * 2.0 ** -24 + EPS[t.dtype]) * want.abs() + TINY
+            assert ((got - want).abs() <= tol * (1 + 2.0 ** -7)).all()
+        if outs is not None:
+            for o in outs:   # nothing past the end
+                end = o.storage_offset() + o.numel()
+                assert (torch.as_strided(o, (9 if o.numel() else 1,), (1,), end) == 5.0).all()
+
+
+def test_clip_extreme_values():
+    for v in (1e30, 1e-30, 3e38):   # squares far outside fp32
+        t = torch.full((1000,), v, device=DEV)
+        s, nrm = clip([t], None, 1.0)
+        want = float(torch.tensor(v).double()) * 1000 ** 0.5
+        assert abs(s - want ** 2) <= 1e-12 * want ** 2 and (abs(nrm - want) <= 1e-6 * want or want > 3.4e38)
+    t = torch.tensor([1.0, float("inf"), 2.0], device=DEV)
+    _, nrm = clip([t], None, 1.0)
+    assert nrm == float("inf") and t[0] == 0 and t[2] == 0 and t[1].isnan()
+    t = torch.tensor([1.0, float("nan"), 2.0], device=DEV)
+    _, nrm = clip([t], None, 1.0)
+    assert nrm != nrm and t.isnan().all()
+
+
+def test_clip_is_reproducible():
+    grads = flat_views([123457, 65, 999999], 1, gen(1))
+    first = clip(grads, [torch.empty_like(t) for t in grads], 0.1)
+    for _ in range(3):
+        assert clip(grads, [torch.empty_like(t) for t in grads], 0.1) == first
+
+
+# ---- the operators together ---------------------------------------------------------------
+def make_layer(seed, Eg=8, El=8, K=256, N=128):
+    g = gen(seed)
+    w13, w2 = bf((El, 2 * N, K), g, 0.08).to(DEV), bf((El, K, N), g, 0.08).to(DEV)
+    emap = None
+    if El < Eg:
+        emap = torch.full((Eg,), -1, dtype=I32)
+        emap[Eg - El:] = torch.arange(El, dtype=I32)
+        emap = emap.to(DEV)
+    return moe.MoeTrainLayer(w13, w2, Eg, emap)
+
+
+def batch(seed, M, K=256, Eg=8, topk=2):
+    g = gen(seed)
+    x, dout = bf((M, K), g), bf((M, K), g, 0.1)
+    ids = torch.stack([torch.randperm(Eg, generator=g)[:topk] for _ in range(max(M, 1))])[:M].to(I32)
+    return x.to(DEV), ids.to(DEV).reshape(M, topk), torch.rand((M, topk), generator=g).to(DEV), dout.to(DEV)
+
+
+def layer_ref(layer, x, ids, tw, dout):
+    """The layer and its gradients in 64 bits, token by token pair, no roundings in between; with every quantity
+    the sum of its terms' magnitudes, which bounds how far one relative 2^-8 in each factor moves it."""
+    d = lambda t: t.detach().cpu().double()
+    w13, w2, X, TW, G = d(layer.w13).requires_grad_(), d(layer.w2).requires_grad_(), d(x).requires_grad_(), \
+        d(tw).requires_grad_(), d(dout)
+    emap = None if layer.expert_map is None else layer.expert_map.tolist()
+    N = layer.N
+    out = torch.zeros(x.shape, dtype=F64)
+    rows = []
+    for t, picks in enumerate(ids.tolist()):
+        acc = torch.zeros(x.shape[1], dtype=F64)
+        for k, i in enumerate(picks):
+            e = i if emap is None else emap[i]
+            if e >= 0:
+                h = w13[e] @ X[t]
+                acc = acc + TW[t, k] * (w2[e] @ (torch.nn.functional.silu(h[:N]) * h[N:]))
+        rows.append(acc)
+    if rows:
+        out = torch.stack(rows)
+        (out * G).sum().backward()
+    z = lambda t: t.grad if t.grad is not None else torch.zeros_like(t)
+    return out.detach(), z(X), z(TW), z(w13), z(w2)
+
+
+def rel(got, ref):
+    got = got.double().cpu()
+    return float((got - ref).norm() / ref.norm().clamp(min=1e-30)) if ref.numel() else 0.0
+
+
+@pytest.mark.parametrize("M,Eg,El,topk", [(1, 8, 8, 2), (37, 8, 8, 2), (64, 8, 4, 3), (300, 8, 8, 1), (0, 8, 8, 2)])
+def test_layer_forward_backward(M, Eg, El, topk):
+    """Against the whole layer in 64 bits.  At most six bf16 roundings (2^-8 each, most far below) lie between the
+    inputs and any output, and each enters linearly, so the 2-norm of the difference stays below 6 * 2^-8 of the
+    result's."""
+    announce("layer", M, Eg, El, topk)
+    layer = make_layer(M + 1, Eg, El)
+    x, ids, tw, dout = batch(M + 2, M, Eg=Eg, topk=topk)
+    out, saved = layer.forward(x, ids, tw)
+    dx, dtw = layer.backward(dout, saved)
+    torch.cuda.synchronize()
+    ref = layer_ref(layer, x, ids, tw, dout)
+    for got, want, what in zip((out, dx, dtw, layer.grad_w13, layer.grad_w2), ref, ("out", "dx", "dtw", "dw13", "dw2")):
+        assert got.shape == want.shape
+        assert rel(got, want) <= 6 * 2.0 ** -8, (what, rel(got, want))
+    # a second batch adds to the weights' gradients
+    before = layer.grad_w2.clone()
+    layer.backward(dout, saved)
+    assert torch.allclose(layer.grad_w2, 2 * before, rtol=2.0 ** -20, atol=1e-30)
+    # and the clip scales both to the norm asked for
+    norm = float(layer.clip_gradients(0.25))
+    total = float((layer.grad_w13.double() ** 2).sum() + (layer.grad_w2.double() ** 2).sum()) ** 0.5
+    if M:
+        assert norm > 0.25 and abs(total - 0.25) <= 0.25 * 2.0 ** -18
+    else:
+        assert norm == 0.0 and total == 0.0
+
+
+def test_layer_interleaved_forwards():
+    """Two forwards before their backwards equal one after the other, bit for bit."""
+    b1, b2 = batch(1, 40), batch(2, 23)
+    l1, l2 = make_layer(9), make_layer(9)
+    o1, s1 = l1.forward(*b1[:3])
+    o2, s2 = l1.forward(*b2[:3])
+    g1, g2 = l1.backward(b1[3], s1), l1.backward(b2[3], s2)
+    p1, t1 = l2.forward(*b1[:3])
+    q1 = l2.backward(b1[3], t1)
+    p2, t2 = l2.forward(*b2[:3])
+    q2 = l2.backward(b2[3], t2)
+    for a, b in ((o1, p1), (o2, p2), *zip(g1, q1), *zip(g2, q2), (l1.grad_w13, l2.grad_w13), (l1.grad_w2, l2.grad_w2)):
+        assert torch.equal(a, b)
+
+
+def test_layer_on_another_stream():
+    layer = make_layer(3)
+    x, ids, tw, dout = batch(4, 50)
+    want, saved = layer.forward(x, ids, tw)
+    wdx, wdt = layer.backward(dout, saved)
+    ww = layer.grad_w13.clone()
+    layer.zero_grad()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        out, saved = layer.forward(x, ids, tw)
+        dx, dt = layer.backward(dout, saved)
+    st.synchronize()
+    assert torch.equal(out, want) and torch.equal(dx, wdx) and torch.equal(dt, wdt) and torch.equal(layer.grad_w13, ww)
+
+
+def test_layer_in_a_graph():
+    """Forward, backward and clip captured once and replayed on new inputs, eager work between the replays."""
+    layer, eager = make_layer(5), make_layer(5)
+    x, ids, tw, dout = batch(6, 48)
+
+    def step(l, *b):
+        l.zero_grad()
+        out, s = l.forward(*b[:3])
+        dx, dt = l.backward(b[3], s)
+        n = l.clip_gradients(0.5)
+        return out, dx, dt, n, l.grad_w13, l.grad_w2
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(layer, x, ids, tw, dout)
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(layer, x, ids, tw, dout)
+    for seed in (6, 7, 8, 9):
+        new = batch(seed, 48)
+        for dst, src in zip((x, ids, tw, dout), new):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(eager, *new)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), seed

@@ -7,6 +7,7 @@ if the library is missing the import of this module fails loudly.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import os
 from typing import Optional
@@ -43,7 +44,9 @@ EXPORTS = ["moe_status_string", "moe_last_error", "moe_max_rows", "moe_grouped_g
            "moe_forward_chunked", "moe_forward_chunked_noalloc", "moe_noalloc_scratch_bytes", "moe_hbm_stream",
            "moe_batched_workspace_size", "moe_experts_batched_masked", "moe_grouped_gemm_fp8_weight_reduce",
            "moe_grouped_gemm_fp8_small", "moe_act_quant_partials", "moe_unpermute_partials",
-           "moe_forward_plan_info"]
+           "moe_forward_plan_info", "moe_permute_bf16", "moe_grouped_gemm_bf16", "moe_grouped_gemm_bf16_dgrad",
+           "moe_grouped_gemm_bf16_wgrad", "moe_silu_mul", "moe_silu_mul_bwd", "moe_unpermute_weight_reduce_bwd",
+           "moe_grad_workspace_size", "moe_grad_sumsq", "moe_grad_clip"]
 
 _lib = None
 
@@ -86,6 +89,16 @@ def load() -> C.CDLL:
                                                          P, P, P, P]
         L.moe_batched_workspace_size.argtypes = [I32, I64, I32, C.POINTER(SZ)]
         L.moe_experts_batched_masked.argtypes = [P, P, P, I32, I64, I32, I32, P, P, P, P, P, P, SZ, P]
+        L.moe_permute_bf16.argtypes = [P, P, I64, I32, I32, P, I32, I32, I32, I64, P, P, P, P, P, P, SZ, P]
+        L.moe_grouped_gemm_bf16.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, P, P]
+        L.moe_grouped_gemm_bf16_dgrad.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, P, P]
+        L.moe_grouped_gemm_bf16_wgrad.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, I32, I32, P, P]
+        L.moe_silu_mul.argtypes = [P, I64, I32, P, P, I32, P, P]
+        L.moe_silu_mul_bwd.argtypes = [P, P, I64, I32, P, P, I32, P, P]
+        L.moe_unpermute_weight_reduce_bwd.argtypes = [P, P, I64, P, P, I64, I32, I32, P, P, P]
+        L.moe_grad_workspace_size.argtypes = [I32, C.POINTER(SZ)]
+        L.moe_grad_sumsq.argtypes = [P, I32, P, P, SZ, P]
+        L.moe_grad_clip.argtypes = [P, I32, P, C.c_float, P, P]
         L.moe_noalloc_scratch_bytes.argtypes = []; L.moe_noalloc_scratch_bytes.restype = SZ
         for name in EXPORTS:
             if name not in ("moe_status_string", "moe_last_error", "moe_max_rows", "moe_grouped_gemm_tile_rows",
@@ -489,3 +502,173 @@ def moe_grouped_gemm_fp8_weight_reduce(a, a_s, w, w_s, expert_offsets, counts, r
                                                      _ptr(inv_perm), _ptr(topk_weights), apply_on_input, Mc, topk,
                                                      _ptr(y), _ptr(counters), _ptr(out), _stream(stream)),
            "moe_grouped_gemm_fp8_weight_reduce")
+
+
+# ---- bf16 experts, forward and backward ------------------------------------------
+MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
+
+
+def moe_permute_bf16(x, topk_ids, expert_map, Eg, El, align, cap_rows, a_perm, counts, expert_offsets, inv_perm,
+                     row_src, workspace, stream=None):
+    """The permute for bf16 rows: a_perm[row] = x[t]; the rest as moe_permute."""
+    check_arg(x, "x", BF16, (None, None))
+    Mc, K = x.shape
+    check_arg(topk_ids, "topk_ids", I32, (Mc, None))
+    topk = topk_ids.shape[1]
+    check_arg(expert_map, "expert_map", I32, (Eg,), optional=True)
+    check_arg(a_perm, "a_perm", BF16, (None, K), min_rows=cap_rows)
+    check_arg(counts, "counts", I32, (El,))
+    check_arg(expert_offsets, "expert_offsets", I32, (El + 1,))
+    check_arg(inv_perm, "inv_perm", I32, (Mc, topk))
+    check_arg(row_src, "row_src", I32, (None,), min_rows=cap_rows)
+    check_arg(workspace, "workspace", (torch.uint8, torch.int32))
+    check_device(x, topk_ids, expert_map, a_perm, counts, expert_offsets, inv_perm, row_src, workspace)
+    _check(load().moe_permute_bf16(_ptr(x), _ptr(topk_ids), Mc, K, topk, _ptr(expert_map), Eg, El, align, cap_rows,
+                                   _ptr(a_perm), _ptr(counts), _ptr(expert_offsets), _ptr(inv_perm), _ptr(row_src),
+                                   _ptr(workspace), _nbytes(workspace), _stream(stream)), "moe_permute_bf16")
+
+
+def _check_segments(expert_offsets, counts, El):
+    check_arg(expert_offsets, "expert_offsets", I32, (El + 1,))
+    check_arg(counts, "counts", I32, (El,))
+
+
+def moe_grouped_gemm_bf16(a, w, expert_offsets, counts, out, rows_hint=0, stream=None):
+    """out[r] = a[r] @ w[e].T over the valid rows r of every expert e."""
+    check_arg(a, "a", BF16, (None, None))
+    cap_rows, k_in = a.shape
+    check_arg(w, "w", BF16, (None, None, k_in))
+    El, n_out, _ = w.shape
+    _check_segments(expert_offsets, counts, El)
+    check_arg(out, "out", BF16, (cap_rows, n_out))
+    check_device(a, w, expert_offsets, counts, out)
+    _check(load().moe_grouped_gemm_bf16(_ptr(a), _ptr(w), _ptr(expert_offsets), _ptr(counts), El, cap_rows, n_out,
+                                        k_in, rows_hint, _ptr(out), _stream(stream)), "moe_grouped_gemm_bf16")
+
+
+def moe_grouped_gemm_bf16_dgrad(dy, w, expert_offsets, counts, dx, rows_hint=0, stream=None):
+    """dx[r] = dy[r] @ w[e] over the valid rows r of every expert e."""
+    check_arg(w, "w", BF16, (None, None, None))
+    El, n_out, k_in = w.shape
+    check_arg(dy, "dy", BF16, (None, n_out))
+    cap_rows = dy.shape[0]
+    _check_segments(expert_offsets, counts, El)
+    check_arg(dx, "dx", BF16, (cap_rows, k_in))
+    check_device(dy, w, expert_offsets, counts, dx)
+    _check(load().moe_grouped_gemm_bf16_dgrad(_ptr(dy), _ptr(w), _ptr(expert_offsets), _ptr(counts), El, cap_rows,
+                                              n_out, k_in, rows_hint, _ptr(dx), _stream(stream)),
+           "moe_grouped_gemm_bf16_dgrad")
+
+
+def moe_grouped_gemm_bf16_wgrad(dy, a, expert_offsets, counts, dw, accumulate=0, rows_hint=0, stream=None):
+    """dw[e] = (or, with accumulate and fp32 dw, +=) dy[rows of e].T @ a[rows of e]."""
+    check_arg(dw, "dw", BF16 + F32, (None, None, None))
+    El, n_out, k_in = dw.shape
+    check_arg(dy, "dy", BF16, (None, n_out))
+    cap_rows = dy.shape[0]
+    check_arg(a, "a", BF16, (cap_rows, k_in))
+    _check_segments(expert_offsets, counts, El)
+    check_device(dy, a, expert_offsets, counts, dw)
+    _check(load().moe_grouped_gemm_bf16_wgrad(_ptr(dy), _ptr(a), _ptr(expert_offsets), _ptr(counts), El, cap_rows,
+                                              n_out, k_in, rows_hint,
+                                              MOE_DTYPE_F32 if dw.dtype == torch.float32 else MOE_DTYPE_BF16,
+                                              int(accumulate), _ptr(dw), _stream(stream)),
+           "moe_grouped_gemm_bf16_wgrad")
+
+
+def _check_silu(h, n, expert_offsets, counts, El):
+    check_arg(h, "h", BF16, (None, 2 * n))
+    check_arg(expert_offsets, "expert_offsets", I32, (El + 1,), optional=True)
+    check_arg(counts, "counts", I32, (El,), optional=True)
+    return h.shape[0]
+
+
+def moe_silu_mul(h, n, act, expert_offsets=None, counts=None, El=0, stream=None):
+    """act = silu(h[:, :n]) * h[:, n:] on the valid rows (all rows without offsets and counts)."""
+    rows = _check_silu(h, n, expert_offsets, counts, El)
+    check_arg(act, "act", BF16, (rows, n))
+    check_device(h, act, expert_offsets, counts)
+    _check(load().moe_silu_mul(_ptr(h), rows, n, _ptr(expert_offsets), _ptr(counts), El, _ptr(act),
+                               _stream(stream)), "moe_silu_mul")
+
+
+def moe_silu_mul_bwd(h, dact, n, dh, expert_offsets=None, counts=None, El=0, stream=None):
+    """Gradient of moe_silu_mul; dh may be h."""
+    rows = _check_silu(h, n, expert_offsets, counts, El)
+    check_arg(dact, "dact", BF16, (rows, n))
+    check_arg(dh, "dh", BF16, (rows, 2 * n))
+    check_device(h, dact, dh, expert_offsets, counts)
+    _check(load().moe_silu_mul_bwd(_ptr(h), _ptr(dact), rows, n, _ptr(expert_offsets), _ptr(counts), El, _ptr(dh),
+                                   _stream(stream)), "moe_silu_mul_bwd")
+
+
+def moe_unpermute_weight_reduce_bwd(dout, y, inv_perm, topk_weights, dy, dweights, stream=None):
+    """Gradient of moe_unpermute_weight_reduce: dy rows and dweights [Mc, topk] from dout."""
+    check_arg(y, "y", BF16, (None, None))
+    y_rows, K = y.shape
+    check_arg(inv_perm, "inv_perm", I32, (None, None))
+    Mc, topk = inv_perm.shape
+    check_arg(dout, "dout", BF16, (Mc, K))
+    check_arg(topk_weights, "topk_weights", F32, (Mc, topk))
+    check_arg(dy, "dy", BF16, (y_rows, K))
+    check_arg(dweights, "dweights", F32, (Mc, topk))
+    check_device(dout, y, inv_perm, topk_weights, dy, dweights)
+    _check(load().moe_unpermute_weight_reduce_bwd(_ptr(dout), _ptr(y), y_rows, _ptr(inv_perm), _ptr(topk_weights),
+                                                  Mc, K, topk, _ptr(dy), _ptr(dweights), _stream(stream)),
+           "moe_unpermute_weight_reduce_bwd")
+
+
+_GRAD_DTYPE = {torch.bfloat16: MOE_DTYPE_BF16, torch.int16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _grad_list(grads, outs):
+    """The moe_grad_tensor array (four 64-bit words a tensor: grad, out, numel, dtype) of a list of tensors."""
+    words = []
+    dev = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        for t in (g,) if o is g else (g, o):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"tensor {i} must be a torch.Tensor, not {type(t).__name__}")
+            if t.dtype not in _GRAD_DTYPE:
+                raise TypeError(f"tensor {i} has dtype {t.dtype}; expected bf16 or float32")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i} must be contiguous")
+            if t.device != dev:
+                raise ValueError(f"tensor {i} is on {t.device}; the library needs tensors on the current CUDA device")
+        if o is not g and (o.shape != g.shape or _GRAD_DTYPE[o.dtype] != _GRAD_DTYPE[g.dtype]):
+            raise ValueError(f"tensor {i}: out has shape {tuple(o.shape)} and dtype {o.dtype}; "
+                             f"expected {tuple(g.shape)} and {g.dtype}")
+        words += (g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_DTYPE[g.dtype])
+    return array.array("Q", words)
+
+
+def moe_grad_workspace_size(num_tensors: int) -> int:
+    n = C.c_size_t(0)
+    _check(load().moe_grad_workspace_size(num_tensors, C.byref(n)), "moe_grad_workspace_size")
+    return int(n.value)
+
+
+def moe_grad_sumsq(grads, sumsq, workspace, stream=None):
+    """sumsq[0] (float64) = the sum of squares of every element of every tensor in grads."""
+    grads = list(grads)
+    check_arg(sumsq, "sumsq", (torch.float64,), (1,))
+    check_arg(workspace, "workspace", (torch.uint8, torch.int32, torch.float64))
+    table = _grad_list(grads, grads)
+    check_device(sumsq, workspace)
+    _check(load().moe_grad_sumsq(C.c_void_p(table.buffer_info()[0]), len(grads), _ptr(sumsq), _ptr(workspace),
+                                 _nbytes(workspace), _stream(stream)), "moe_grad_sumsq")
+
+
+def moe_grad_clip(grads, outs, sumsq, max_norm, norm=None, stream=None):
+    """outs[i] = grads[i] * min(1, max_norm / (sqrt(sumsq) + 1e-6)); outs None: in place.  norm [1] float32
+    receives the norm before clipping."""
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} outs for {len(grads)} grads")
+    check_arg(sumsq, "sumsq", (torch.float64,), (1,))
+    check_arg(norm, "norm", F32, (1,), optional=True)
+    table = _grad_list(grads, outs)
+    check_device(sumsq, norm)
+    _check(load().moe_grad_clip(C.c_void_p(table.buffer_info()[0]), len(grads), _ptr(sumsq), max_norm, _ptr(norm),
+                                _stream(stream)), "moe_grad_clip")

@@ -4,9 +4,11 @@
 // Every entry point validates its arguments before enqueuing anything, so a
 // bad call leaves the stream untouched.  Nothing here allocates, frees or
 // synchronises device memory.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -300,21 +302,17 @@ int moe_count(const int32_t* topk_ids, int64_t num_pairs, const int32_t* expert_
 
 namespace {
 
-// moe_permute (quant false: a_q / a_s given) and moe_quant_permute (quant
-// true: x given): the same checks, then the launch
-int permute_common(bool quant, const uint8_t* a_q, const float* a_s, const uint16_t* x, const int32_t* topk_ids,
-                   const float* topk_weights, int32_t apply_on_input, int64_t Mc, int32_t K, int32_t topk,
-                   const int32_t* expert_map, int32_t Eg, int32_t El, int32_t align, int64_t cap_rows,
-                   uint8_t* a_perm, float* a_perm_s, int32_t* counts, int32_t* expert_offsets,
-                   int32_t* inv_perm, int32_t* row_src, void* workspace, size_t workspace_bytes,
-                   void* stream) {
+// What every permute entry point checks: sizes, the outputs that an empty
+// chunk writes too, the expert map and the workspace.
+int check_permute(int64_t Mc, int32_t K, int32_t topk, const int32_t* expert_map, int32_t Eg, int32_t El,
+                  int32_t align, int64_t cap_rows, const int32_t* counts, const int32_t* expert_offsets,
+                  const int32_t* row_src, const void* workspace, size_t workspace_bytes) {
     REQUIRE(Mc >= 0, MOE_ERR_SHAPE, "Mc < 0");
     REQUIRE(K > 0 && K % moe::kGroup == 0, MOE_ERR_SHAPE, "K=%d is not a positive multiple of 128", K);
     REQUIRE(topk >= 1 && topk <= 256, MOE_ERR_SHAPE, "topk=%d outside [1,256]", topk);
     REQUIRE(Eg >= 1 && El >= 1 && El <= moe::kMaxLocalExperts, MOE_ERR_SHAPE, "Eg=%d El=%d", Eg, El);
     REQUIRE(expert_map != nullptr || El <= Eg, MOE_ERR_SHAPE, "El > Eg without an expert map");
     REQUIRE(valid_align(align), MOE_ERR_SHAPE, "align=%d not in {16,32,64,128}", align);
-    REQUIRE(apply_on_input == 0 || apply_on_input == 1, MOE_ERR_INVALID_ARG, "apply_on_input=%d", apply_on_input);
     REQUIRE(Mc * topk < (int64_t(1) << 31) && cap_rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "too many rows");
     const int64_t need_rows = max_rows(Mc, topk, El, align);
     REQUIRE(cap_rows >= need_rows, MOE_ERR_WORKSPACE_TOO_SMALL, "cap_rows=%lld < %lld",
@@ -327,6 +325,22 @@ int permute_common(bool quant, const uint8_t* a_q, const float* a_s, const uint1
     REQUIRE_PTR(counts);
     REQUIRE_PTR(expert_offsets);
     if (cap_rows > 0) REQUIRE_PTR(row_src);
+    REQUIRE(expert_map == nullptr || aligned16(expert_map), MOE_ERR_INVALID_ARG, "expert_map alignment");
+    return MOE_OK;
+}
+
+// moe_permute (quant false: a_q / a_s given) and moe_quant_permute (quant
+// true: x given): the same checks, then the launch
+int permute_common(bool quant, const uint8_t* a_q, const float* a_s, const uint16_t* x, const int32_t* topk_ids,
+                   const float* topk_weights, int32_t apply_on_input, int64_t Mc, int32_t K, int32_t topk,
+                   const int32_t* expert_map, int32_t Eg, int32_t El, int32_t align, int64_t cap_rows,
+                   uint8_t* a_perm, float* a_perm_s, int32_t* counts, int32_t* expert_offsets,
+                   int32_t* inv_perm, int32_t* row_src, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+    int st = check_permute(Mc, K, topk, expert_map, Eg, El, align, cap_rows, counts, expert_offsets, row_src,
+                           workspace, workspace_bytes);
+    if (st) return st;
+    REQUIRE(apply_on_input == 0 || apply_on_input == 1, MOE_ERR_INVALID_ARG, "apply_on_input=%d", apply_on_input);
     if (Mc > 0) {
         if (quant) {
             REQUIRE_PTR(x);
@@ -341,8 +355,7 @@ int permute_common(bool quant, const uint8_t* a_q, const float* a_s, const uint1
         REQUIRE_PTR(inv_perm);
         if (apply_on_input) REQUIRE_PTR(topk_weights);
     }
-    REQUIRE(expert_map == nullptr || aligned16(expert_map), MOE_ERR_INVALID_ARG, "expert_map alignment");
-    int st = check_device(nullptr);
+    st = check_device(nullptr);
     if (st) return st;
     if (quant)
         HIP_OK(moe::launch_quant_permute(x, topk_ids, topk_weights, apply_on_input, Mc, K, topk, expert_map, Eg,
@@ -924,6 +937,289 @@ int moe_experts_batched_masked(const uint8_t* a_q, const float* a_s, const int32
                                         moe::gemm_tile_rows(rows, El), cus, s));
     HIP_OK(moe::launch_grouped_gemm(act_q, act_s, w2, w2_s, offsets, cut, El, rows, K, N, out,
                                     moe::gemm_tile_rows(rows, El), cus, s));
+    return MOE_OK;
+}
+
+int moe_permute_bf16(const uint16_t* x, const int32_t* topk_ids, int64_t Mc, int32_t K, int32_t topk,
+                     const int32_t* expert_map, int32_t Eg, int32_t El, int32_t align, int64_t cap_rows,
+                     uint16_t* a_perm, int32_t* counts, int32_t* expert_offsets, int32_t* inv_perm,
+                     int32_t* row_src, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_permute(Mc, K, topk, expert_map, Eg, El, align, cap_rows, counts, expert_offsets, row_src,
+                           workspace, workspace_bytes);
+    if (st) return st;
+    REQUIRE(K <= 65536, MOE_ERR_SHAPE, "K=%d > 65536", K);
+    if (Mc > 0) {
+        REQUIRE_PTR(x);
+        REQUIRE_PTR(topk_ids);
+        REQUIRE_PTR(a_perm);
+        REQUIRE_PTR(inv_perm);
+    }
+    REQUIRE(!overlaps(x, (size_t)Mc * K * 2, a_perm, (size_t)cap_rows * K * 2), MOE_ERR_INVALID_ARG,
+            "a_perm overlaps x");
+    st = check_device(nullptr);
+    if (st) return st;
+    HIP_OK(moe::launch_permute_bf16(x, topk_ids, Mc, K, topk, expert_map, Eg, El, align, cap_rows, a_perm, counts,
+                                    expert_offsets, inv_perm, row_src, static_cast<int32_t*>(workspace),
+                                    static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the three grouped bf16 products check alike.
+int check_gemm_bf16(const int32_t* expert_offsets, const int32_t* counts, int32_t El, int64_t cap_rows,
+                    int32_t n_out, int32_t k_in) {
+    REQUIRE(El >= 1 && El <= moe::kMaxLocalExperts, MOE_ERR_SHAPE, "El=%d outside [1,1024]", El);
+    REQUIRE(cap_rows >= 0 && cap_rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "cap_rows=%lld", (long long)cap_rows);
+    REQUIRE(n_out > 0 && n_out % 8 == 0 && n_out <= 65536, MOE_ERR_SHAPE,
+            "n_out=%d is not a positive multiple of 8 up to 65536", n_out);
+    REQUIRE(k_in > 0 && k_in % 8 == 0 && k_in <= 65536, MOE_ERR_SHAPE,
+            "k_in=%d is not a positive multiple of 8 up to 65536", k_in);
+    REQUIRE_PTR(expert_offsets);
+    REQUIRE_PTR(counts);
+    return MOE_OK;
+}
+
+// SiLU-mul and its gradient: the row set
+int check_silu(int64_t rows, int32_t n, const int32_t* expert_offsets, const int32_t* counts, int32_t El) {
+    REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "rows=%lld", (long long)rows);
+    REQUIRE(n > 0 && n % 8 == 0 && n <= 65536, MOE_ERR_SHAPE, "n=%d is not a positive multiple of 8 up to 65536", n);
+    REQUIRE((expert_offsets == nullptr) == (counts == nullptr), MOE_ERR_INVALID_ARG,
+            "expert_offsets and counts must both be given or both be NULL");
+    if (expert_offsets) {
+        REQUIRE(El >= 1 && El <= moe::kMaxLocalExperts, MOE_ERR_SHAPE, "El=%d outside [1,1024]", El);
+        REQUIRE_PTR(expert_offsets);
+        REQUIRE_PTR(counts);
+    }
+    return MOE_OK;
+}
+
+int check_grads(const moe_grad_tensor* t, int32_t num, bool clip) {
+    REQUIRE(num >= 0 && num <= (1 << 20), MOE_ERR_SHAPE, "num_tensors=%d outside [0, 2^20]", num);
+    REQUIRE(num == 0 || t != nullptr, MOE_ERR_INVALID_ARG, "tensors is NULL");
+    for (int32_t i = 0; i < num; ++i) {
+        REQUIRE(t[i].dtype == MOE_DTYPE_BF16 || t[i].dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG,
+                "tensor %d: dtype=%d", i, t[i].dtype);
+        REQUIRE(t[i].reserved == 0, MOE_ERR_INVALID_ARG, "tensor %d: reserved=%d", i, t[i].reserved);
+        REQUIRE(t[i].numel >= 0 && t[i].numel <= (int64_t(1) << 40), MOE_ERR_SHAPE, "tensor %d: numel=%lld", i,
+                (long long)t[i].numel);
+        const uintptr_t es = t[i].dtype == MOE_DTYPE_F32 ? 4 : 2;
+        const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), o = reinterpret_cast<uintptr_t>(t[i].out);
+        if (t[i].numel > 0) {
+            REQUIRE(g != 0 && g % es == 0, MOE_ERR_INVALID_ARG, "tensor %d: grad is NULL or not aligned to its element", i);
+            if (clip) {
+                REQUIRE(o != 0 && o % es == 0, MOE_ERR_INVALID_ARG,
+                        "tensor %d: out is NULL or not aligned to its element", i);
+                REQUIRE(o == g || !overlaps(t[i].grad, t[i].numel * es, t[i].out, t[i].numel * es),
+                        MOE_ERR_INVALID_ARG, "tensor %d: out overlaps grad without being it", i);
+            }
+        }
+    }
+    return MOE_OK;
+}
+
+// Refuses a clip list in which memory that one tensor's `out` covers is any
+// other tensor's grad or out: the result would depend on which block comes
+// first.  The same gradient read twice is fine.
+int check_grad_overlap(const moe_grad_tensor* t, int32_t num) {
+    struct Span {
+        uintptr_t lo, hi;
+        int32_t i;
+        bool write;
+    };
+    Span* v = num > 0 ? static_cast<Span*>(std::malloc(2 * (size_t)num * sizeof(Span))) : nullptr;
+    REQUIRE(num == 0 || v != nullptr, MOE_ERR_INVALID_ARG, "no host memory for a list of %d tensors", num);
+    int n = 0;
+    for (int32_t i = 0; i < num; ++i) {
+        const uintptr_t bytes = (uintptr_t)t[i].numel * (t[i].dtype == MOE_DTYPE_F32 ? 4 : 2);
+        const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), o = reinterpret_cast<uintptr_t>(t[i].out);
+        if (bytes == 0) continue;
+        v[n++] = Span{o, o + bytes, i, true};
+        if (g != o) v[n++] = Span{g, g + bytes, i, false};
+    }
+    std::sort(v, v + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    uintptr_t any = 0, written = 0;   // ends of the furthest span and written span so far
+    int32_t bad = -1;
+    for (int j = 0; j < n && bad < 0; ++j) {
+        if (v[j].lo < (v[j].write ? any : written)) bad = v[j].i;
+        any = v[j].hi > any ? v[j].hi : any;
+        if (v[j].write) written = v[j].hi > written ? v[j].hi : written;
+    }
+    std::free(v);
+    REQUIRE(bad < 0, MOE_ERR_INVALID_ARG, "tensor %d: its memory overlaps another tensor's that is written", bad);
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_grouped_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* expert_offsets,
+                          const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out, int32_t k_in,
+                          int64_t rows_hint, uint16_t* out, void* stream) {
+    int st = check_gemm_bf16(expert_offsets, counts, El, cap_rows, n_out, k_in);
+    if (st) return st;
+    if (cap_rows == 0) return MOE_OK;
+    REQUIRE_PTR(a);
+    REQUIRE_PTR(w);
+    REQUIRE_PTR(out);
+    const size_t out_b = (size_t)cap_rows * n_out * 2;
+    REQUIRE(!overlaps(out, out_b, a, (size_t)cap_rows * k_in * 2) && !overlaps(out, out_b, w, (size_t)El * n_out * k_in * 2),
+            MOE_ERR_INVALID_ARG, "out overlaps an input");
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_gemm_bf16(a, w, expert_offsets, counts, El, cap_rows, n_out, k_in,
+                                 rows_hint > 0 ? rows_hint : cap_rows, out, cus, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int32_t* expert_offsets,
+                                const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out,
+                                int32_t k_in, int64_t rows_hint, uint16_t* dx, void* stream) {
+    int st = check_gemm_bf16(expert_offsets, counts, El, cap_rows, n_out, k_in);
+    if (st) return st;
+    if (cap_rows == 0) return MOE_OK;
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(w);
+    REQUIRE_PTR(dx);
+    const size_t dx_b = (size_t)cap_rows * k_in * 2;
+    REQUIRE(!overlaps(dx, dx_b, dy, (size_t)cap_rows * n_out * 2) && !overlaps(dx, dx_b, w, (size_t)El * n_out * k_in * 2),
+            MOE_ERR_INVALID_ARG, "dx overlaps an input");
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_gemm_bf16_dgrad(dy, w, expert_offsets, counts, El, cap_rows, n_out, k_in,
+                                       rows_hint > 0 ? rows_hint : cap_rows, dx, cus,
+                                       static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* expert_offsets,
+                                const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out,
+                                int32_t k_in, int64_t rows_hint, int32_t dw_dtype, int32_t accumulate, void* dw,
+                                void* stream) {
+    int st = check_gemm_bf16(expert_offsets, counts, El, cap_rows, n_out, k_in);
+    if (st) return st;
+    REQUIRE(dw_dtype == MOE_DTYPE_BF16 || dw_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG, "dw_dtype=%d", dw_dtype);
+    REQUIRE(accumulate == 0 || (accumulate == 1 && dw_dtype == MOE_DTYPE_F32), MOE_ERR_INVALID_ARG,
+            "accumulate=%d: 0, or 1 with fp32 dw", accumulate);
+    if (cap_rows > 0) {   // without rows dw is all zeros, or as it was
+        REQUIRE_PTR(dy);
+        REQUIRE_PTR(a);
+    }
+    REQUIRE_PTR(dw);
+    const size_t dw_b = (size_t)El * n_out * k_in * (dw_dtype == MOE_DTYPE_F32 ? 4 : 2);
+    REQUIRE(!overlaps(dw, dw_b, dy, (size_t)cap_rows * n_out * 2) && !overlaps(dw, dw_b, a, (size_t)cap_rows * k_in * 2),
+            MOE_ERR_INVALID_ARG, "dw overlaps an input");
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_gemm_bf16_wgrad(dy, a, expert_offsets, counts, El, cap_rows, n_out, k_in,
+                                       rows_hint > 0 ? rows_hint : cap_rows, dw_dtype == MOE_DTYPE_F32,
+                                       accumulate != 0, dw, cus, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_silu_mul(const uint16_t* h, int64_t rows, int32_t n, const int32_t* expert_offsets,
+                 const int32_t* counts, int32_t El, uint16_t* act, void* stream) {
+    int st = check_silu(rows, n, expert_offsets, counts, El);
+    if (st) return st;
+    if (rows == 0) return MOE_OK;
+    REQUIRE_PTR(h);
+    REQUIRE_PTR(act);
+    REQUIRE(!overlaps(act, (size_t)rows * n * 2, h, (size_t)rows * n * 4), MOE_ERR_INVALID_ARG, "act overlaps h");
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_silu_mul(h, rows, n, expert_offsets, counts, El, act, cus, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_silu_mul_bwd(const uint16_t* h, const uint16_t* dact, int64_t rows, int32_t n,
+                     const int32_t* expert_offsets, const int32_t* counts, int32_t El, uint16_t* dh,
+                     void* stream) {
+    int st = check_silu(rows, n, expert_offsets, counts, El);
+    if (st) return st;
+    if (rows == 0) return MOE_OK;
+    REQUIRE_PTR(h);
+    REQUIRE_PTR(dact);
+    REQUIRE_PTR(dh);
+    const size_t h_b = (size_t)rows * n * 4;
+    REQUIRE(dh == h || !overlaps(dh, h_b, h, h_b), MOE_ERR_INVALID_ARG, "dh overlaps h without being it");
+    REQUIRE(!overlaps(dh, h_b, dact, (size_t)rows * n * 2), MOE_ERR_INVALID_ARG, "dh overlaps dact");
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_silu_mul_bwd(h, dact, rows, n, expert_offsets, counts, El, dh, cus,
+                                    static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows,
+                                    const int32_t* inv_perm, const float* topk_weights, int64_t Mc, int32_t K,
+                                    int32_t topk, uint16_t* dy, float* dweights, void* stream) {
+    REQUIRE(Mc >= 0 && y_rows >= 0 && y_rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "Mc=%lld y_rows=%lld",
+            (long long)Mc, (long long)y_rows);
+    REQUIRE(K > 0 && K % moe::kGroup == 0, MOE_ERR_SHAPE, "K=%d is not a positive multiple of 128", K);
+    REQUIRE(topk >= 1 && topk <= 256, MOE_ERR_SHAPE, "topk=%d outside [1,256]", topk);
+    REQUIRE(Mc < (int64_t(1) << 31) / topk, MOE_ERR_SHAPE, "too many tokens");
+    if (Mc == 0) return MOE_OK;
+    REQUIRE_PTR(dout);
+    REQUIRE_PTR(inv_perm);
+    REQUIRE_PTR(topk_weights);
+    REQUIRE_PTR(dweights);
+    if (y_rows > 0) {
+        REQUIRE_PTR(y);
+        REQUIRE_PTR(dy);
+    }
+    const size_t y_b = (size_t)y_rows * K * 2;
+    REQUIRE(!overlaps(dy, y_b, y, y_b) && !overlaps(dy, y_b, dout, (size_t)Mc * K * 2), MOE_ERR_INVALID_ARG,
+            "dy overlaps an input");
+    int cus = 0;
+    int st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_unpermute_bwd(dout, y, y_rows, inv_perm, topk_weights, Mc, K, topk, dy, dweights, cus,
+                                     static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_grad_workspace_size(int32_t num_tensors, size_t* bytes) {
+    REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "bytes is NULL");
+    REQUIRE(num_tensors >= 0 && num_tensors <= (1 << 20), MOE_ERR_SHAPE, "num_tensors=%d outside [0, 2^20]",
+            num_tensors);
+    *bytes = moe::grad_workspace(num_tensors > 0 ? num_tensors : 1);
+    return MOE_OK;
+}
+
+int moe_grad_sumsq(const moe_grad_tensor* tensors, int32_t num_tensors, double* sumsq, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    int st = check_grads(tensors, num_tensors, false);
+    if (st) return st;
+    REQUIRE_PTR(sumsq);
+    REQUIRE_PTR(workspace);
+    const size_t need = moe::grad_workspace(num_tensors > 0 ? num_tensors : 1);
+    REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+    st = check_device(nullptr);
+    if (st) return st;
+    HIP_OK(moe::launch_grad_sumsq(tensors, num_tensors, sumsq, static_cast<double*>(workspace),
+                                  static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_grad_clip(const moe_grad_tensor* tensors, int32_t num_tensors, const double* sumsq, float max_norm,
+                  float* norm, void* stream) {
+    int st = check_grads(tensors, num_tensors, true);
+    if (!st) st = check_grad_overlap(tensors, num_tensors);
+    if (st) return st;
+    REQUIRE(max_norm >= 0.0f, MOE_ERR_INVALID_ARG, "max_norm=%g is negative or NaN", (double)max_norm);
+    REQUIRE_PTR(sumsq);
+    if (norm) REQUIRE_PTR(norm);
+    st = check_device(nullptr);
+    if (st) return st;
+    HIP_OK(moe::launch_grad_clip(tensors, num_tensors, sumsq, max_norm, norm, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

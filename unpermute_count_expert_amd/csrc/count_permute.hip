@@ -594,7 +594,7 @@ __global__ __launch_bounds__(kPermThreads) void k_permute_scatter(
         }
     }
     if constexpr (!QUANT) {
-        for (int tl = wave; tl < ntok; tl += kWaves) {
+        for (int tl = wave; a_s != nullptr && tl < ntok; tl += kWaves) {   // bf16 rows have no scales
             const int64_t t = t0 + tl;
             const int* rm = rowmap + tl * topk;
             for (int g = g_lo + lane; g < g_lo + ng; g += kWave) {
@@ -697,6 +697,16 @@ hipError_t launch_permute(const uint8_t* a_q, const float* a_s, const int32_t* i
         a_q, a_s, nullptr, ids, topk_w, apply_on_input, Mc, K, topk, tpb, emap, Eg, El, bits_for(El), hist,
         counts, counts_copy, align, cap_rows, offsets, a_perm, a_perm_s, inv_perm, row_src);
     return hipGetLastError();
+}
+
+// A bf16 row is 2K bytes to copy, in 128-byte groups like a row of codes.
+hipError_t launch_permute_bf16(const uint16_t* x, const int32_t* ids, int64_t Mc, int K, int topk,
+                               const int32_t* emap, int Eg, int El, int align, int64_t cap_rows, uint16_t* a_perm,
+                               int32_t* counts, int32_t* offsets, int32_t* inv_perm, int32_t* row_src, int32_t* hist,
+                               hipStream_t s) {
+    return launch_permute(reinterpret_cast<const uint8_t*>(x), nullptr, ids, nullptr, 0, Mc, 2 * K, topk, emap, Eg,
+                          El, align, cap_rows, reinterpret_cast<uint8_t*>(a_perm), nullptr, counts, offsets, inv_perm,
+                          row_src, hist, nullptr, s);
 }
 
 hipError_t launch_quant_permute(const uint16_t* x, const int32_t* ids, const float* topk_w, int apply_on_input,

@@ -1,0 +1,208 @@
+// grad_clip.hip -- global gradient norm over many tensors, and clipping, for
+// gfx950:
+//
+//   S = sum over tensors and elements of g^2,
+//   c = min(1, max_norm / (sqrt(S) + 1e-6)),  out = g c.
+//
+// Squares and sums are fp64: the square of any fp32 value is exact enough
+// there and neither overflows nor vanishes, and the kernel still runs at the
+// rate of the reads.  No atomics: every block writes one partial sum, one
+// block adds the partials in a fixed order, so equal calls give equal bits.
+// The tensor list goes by value in the kernel arguments (a launch holds up to
+// 64 tensors), so nothing is copied to the device and a captured graph keeps
+// it.
+#include "moe_device.hpp"
+#include "moe_internal.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 16;                          // bytes per lane and load
+constexpr int kChunk = 4 * kThreads * kVec;       // bytes of one work item
+
+struct List {
+    const void* grad[kGradTensors];
+    void* out[kGradTensors];
+    int64_t numel[kGradTensors];
+    int32_t first[kGradTensors + 1];   // work items before tensor i
+    uint64_t f32;                      // bit i: tensor i is fp32, else bf16
+    int num;
+};
+static_assert(sizeof(List) <= 3072, "fits the kernel arguments");
+
+// The work item's tensor (uniform over the block) and byte range, aligned
+// down to 16 bytes in memory at both ends but the tensor's own.
+struct Item {
+    int i;
+    int es;              // element size
+    uintptr_t g, lo, hi; // tensor start, this item's bytes [lo, hi)
+};
+
+__device__ __forceinline__ Item item_of(const List& L, int64_t q) {
+    int lo = 0, hi = L.num - 1;   // the last tensor with first[i] <= q
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (L.first[mid] <= q) lo = mid; else hi = mid - 1;
+    }
+    Item it;
+    it.i = lo;
+    it.es = (L.f32 >> lo) & 1 ? 4 : 2;
+    it.g = reinterpret_cast<uintptr_t>(L.grad[lo]);
+    const uintptr_t end = it.g + (uintptr_t)L.numel[lo] * it.es;
+    const uintptr_t base = (it.g & ~uintptr_t(kVec - 1)) + (uintptr_t)(q - L.first[lo]) * kChunk;
+    it.lo = base < it.g ? it.g : base;
+    it.hi = base + kChunk < end ? base + kChunk : end;
+    return it;
+}
+
+// sum of squares of the elements in a 16-byte vector
+__device__ __forceinline__ double sq16(const uint4& v, bool f32) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (f32) {
+            const double x = __uint_as_float(u[i]);
+            s = __builtin_fma(x, x, s);
+        } else {
+            const double x = __uint_as_float(u[i] << 16), y = __uint_as_float(u[i] & 0xffff0000u);
+            s = __builtin_fma(x, x, s);
+            s = __builtin_fma(y, y, s);
+        }
+    }
+    return s;
+}
+
+__device__ __forceinline__ float load_el(uintptr_t p, int es) {
+    return es == 4 ? *reinterpret_cast<const float*>(p) : bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double s_w[kThreads / kWave];
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, kWave);
+    if ((threadIdx.x & (kWave - 1)) == 0) s_w[threadIdx.x / kWave] = v;
+    __syncthreads();
+    double r = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) r += s_w[w];
+    return r;
+}
+
+__global__ __launch_bounds__(kThreads) void k_sumsq(List L, double* __restrict__ partials) {
+    double acc = 0.0;
+    for (int64_t q = blockIdx.x; q < L.first[L.num]; q += gridDim.x) {
+        const Item it = item_of(L, q);
+        const uintptr_t vlo = (it.lo + kVec - 1) & ~uintptr_t(kVec - 1), vhi = it.hi & ~uintptr_t(kVec - 1);
+        for (uintptr_t p = vlo + threadIdx.x * kVec; p < vhi; p += kThreads * kVec)
+            acc += sq16(*reinterpret_cast<const uint4*>(p), it.es == 4);
+        // ragged ends of the tensor: at most 7 elements each (with no whole
+        // vector between them the two meet at vlo or vhi)
+        const uintptr_t head = vlo < it.hi ? vlo : it.hi, tail = vhi > head ? vhi : head;
+        for (uintptr_t p = it.lo + threadIdx.x * it.es; p < head; p += kThreads * it.es) {
+            const double x = load_el(p, it.es);
+            acc = __builtin_fma(x, x, acc);
+        }
+        for (uintptr_t p = tail + threadIdx.x * it.es; p < it.hi; p += kThreads * it.es) {
+            const double x = load_el(p, it.es);
+            acc = __builtin_fma(x, x, acc);
+        }
+    }
+    const double s = block_sum(acc);
+    if (threadIdx.x == 0) partials[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_sum_partials(const double* __restrict__ partials, int num,
+                                                           double* __restrict__ sumsq) {
+    double acc = 0.0;
+    for (int i = threadIdx.x; i < num; i += kThreads) acc += partials[i];
+    const double s = block_sum(acc);
+    if (threadIdx.x == 0) sumsq[0] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_clip(List L, const double* __restrict__ sumsq, float max_norm,
+                                                   float* __restrict__ norm) {
+    const float nrm = (float)__builtin_sqrt(sumsq[0]);
+    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = nrm;
+    const float ratio = max_norm / (nrm + 1e-6f);
+    const float c = ratio >= 1.0f ? 1.0f : ratio;   // a NaN ratio stays NaN
+    for (int64_t q = blockIdx.x; q < L.first[L.num]; q += gridDim.x) {
+        const Item it = item_of(L, q);
+        const uintptr_t o = reinterpret_cast<uintptr_t>(L.out[it.i]);
+        if (o == it.g && c == 1.0f) continue;
+        const bool f32 = it.es == 4;
+        auto one = [&](uintptr_t p) {
+            const float v = load_el(p, it.es) * c;
+            if (f32) *reinterpret_cast<float*>(o + (p - it.g)) = v;
+            else *reinterpret_cast<uint16_t*>(o + (p - it.g)) = f32_to_bf16(v);
+        };
+        if (((o - it.g) & (kVec - 1)) != 0) {   // the two are not aligned alike
+            for (uintptr_t p = it.lo + threadIdx.x * it.es; p < it.hi; p += kThreads * it.es) one(p);
+            continue;
+        }
+        const uintptr_t vlo = (it.lo + kVec - 1) & ~uintptr_t(kVec - 1), vhi = it.hi & ~uintptr_t(kVec - 1);
+        for (uintptr_t p = vlo + threadIdx.x * kVec; p < vhi; p += kThreads * kVec) {
+            uint4 v = *reinterpret_cast<const uint4*>(p);
+            uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = f32 ? __float_as_uint(__uint_as_float(u[i]) * c)
+                           : f32x2_to_bf16x2(__uint_as_float(u[i] << 16) * c, __uint_as_float(u[i] & 0xffff0000u) * c);
+            store_once16(reinterpret_cast<void*>(o + (p - it.g)), uint4{u[0], u[1], u[2], u[3]});
+        }
+        const uintptr_t head = vlo < it.hi ? vlo : it.hi, tail = vhi > head ? vhi : head;
+        for (uintptr_t p = it.lo + threadIdx.x * it.es; p < head; p += kThreads * it.es) one(p);
+        for (uintptr_t p = tail + threadIdx.x * it.es; p < it.hi; p += kThreads * it.es) one(p);
+    }
+}
+
+// The next launch's tensors and its grid; a tensor's work items are the
+// kChunk-byte windows, from its 16-byte aligned-down start, that it touches.
+int64_t fill(List& L, const moe_grad_tensor* t, int num) {
+    L.num = num;
+    L.f32 = 0;
+    int64_t items = 0;
+    for (int i = 0; i < num; ++i) {
+        L.grad[i] = t[i].grad;
+        L.out[i] = t[i].out;
+        L.numel[i] = t[i].numel;
+        L.first[i] = (int32_t)items;
+        const bool f32 = t[i].dtype == MOE_DTYPE_F32;
+        L.f32 |= (uint64_t)f32 << i;
+        const int64_t bytes = t[i].numel * (f32 ? 4 : 2);
+        const int64_t skew = (int64_t)(reinterpret_cast<uintptr_t>(t[i].grad) & (kVec - 1));
+        if (bytes > 0) items += (skew + bytes + kChunk - 1) / kChunk;
+    }
+    L.first[num] = (int32_t)items;
+    return items;
+}
+
+}  // namespace
+
+hipError_t launch_grad_sumsq(const moe_grad_tensor* t, int num, double* sumsq, double* partials, hipStream_t s) {
+    int np = 0;
+    for (int i = 0; i < num; i += kGradTensors) {
+        List L;
+        const int64_t items = fill(L, t + i, num - i < kGradTensors ? num - i : kGradTensors);
+        const int grid = (int)(items < kGradBlocks ? items : kGradBlocks);
+        if (grid == 0) continue;
+        k_sumsq<<<grid, kThreads, 0, s>>>(L, partials + np);
+        np += grid;
+    }
+    k_sum_partials<<<1, kThreads, 0, s>>>(partials, np, sumsq);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const moe_grad_tensor* t, int num, const double* sumsq, float max_norm, float* norm,
+                            hipStream_t s) {
+    for (int i = 0; i < num || i == 0; i += kGradTensors) {
+        List L;
+        const int64_t items = fill(L, t + i, num - i < kGradTensors ? num - i : kGradTensors);
+        const int grid = (int)(items < kGradBlocks ? (items > 0 ? items : 1) : kGradBlocks);
+        k_clip<<<grid, kThreads, 0, s>>>(L, sumsq, max_norm, i == 0 ? norm : nullptr);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe

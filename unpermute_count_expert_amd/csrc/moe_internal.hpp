@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "moe.h"
+
 namespace moe {
 
 constexpr int MOE_ACT_IDENTITY_K = 0;  // same values as MOE_ACT_* in moe.h
@@ -147,6 +149,44 @@ hipError_t launch_unpermute_part(const float* part, const int32_t* info, int64_t
                                  const int32_t* offsets, const int32_t* counts, int El, int64_t y_rows,
                                  const int32_t* inv_perm, const float* topk_w, int64_t Mc, int K, int topk,
                                  int apply_on_input, uint16_t* out, hipStream_t s);
+
+// ---- bf16 experts and their gradients -------------------------------------------
+// The permute of bf16 rows: launch_permute's indices and row copies.
+hipError_t launch_permute_bf16(const uint16_t* x, const int32_t* ids, int64_t Mc, int K, int topk,
+                               const int32_t* emap, int Eg, int El, int align, int64_t cap_rows, uint16_t* a_perm,
+                               int32_t* counts, int32_t* offsets, int32_t* inv_perm, int32_t* row_src, int32_t* hist,
+                               hipStream_t s);
+
+// The three grouped products over the experts' valid rows; rows_hint > 0.
+hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* offsets, const int32_t* counts,
+                            int El, int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, uint16_t* out,
+                            int num_cus, hipStream_t s);
+hipError_t launch_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int32_t* offsets,
+                                  const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
+                                  int64_t rows_hint, uint16_t* dx, int num_cus, hipStream_t s);
+hipError_t launch_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* offsets,
+                                  const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
+                                  int64_t rows_hint, bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s);
+
+hipError_t launch_silu_mul(const uint16_t* h, int64_t rows, int n, const int32_t* offsets, const int32_t* counts,
+                           int El, uint16_t* act, int num_cus, hipStream_t s);
+hipError_t launch_silu_mul_bwd(const uint16_t* h, const uint16_t* dact, int64_t rows, int n, const int32_t* offsets,
+                               const int32_t* counts, int El, uint16_t* dh, int num_cus, hipStream_t s);
+
+hipError_t launch_unpermute_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows, const int32_t* inv_perm,
+                                const float* topk_w, int64_t Mc, int K, int topk, uint16_t* dy, float* dweights,
+                                int num_cus, hipStream_t s);
+
+// Tensors of one launch of the gradient kernels; each fills at most
+// kGradBlocks blocks and partial sums.
+constexpr int kGradTensors = 64;
+constexpr int kGradBlocks = 2048;
+inline size_t grad_workspace(int num_tensors) {
+    return (size_t)((num_tensors + kGradTensors - 1) / kGradTensors) * kGradBlocks * sizeof(double);
+}
+hipError_t launch_grad_sumsq(const moe_grad_tensor* t, int num, double* sumsq, double* partials, hipStream_t s);
+hipError_t launch_grad_clip(const moe_grad_tensor* t, int num, const double* sumsq, float max_norm, float* norm,
+                            hipStream_t s);
 
 // ---- HBM streams (measured ceilings) -------------------------------------------
 // mode: MOE_STREAM_* of moe.h; sink receives nothing in practice (read mode
