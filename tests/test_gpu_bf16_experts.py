@@ -517,10 +517,17 @@ def test_layer_forward_backward(M, Eg, El, topk):
     for got, want, what in zip((out, dx, dtw, layer.grad_w13, layer.grad_w2), ref, ("out", "dx", "dtw", "dw13", "dw2")):
         assert got.shape == want.shape
         assert rel(got, want) <= 6 * 2.0 ** -8, (what, rel(got, want))
-    # a second batch adds to the weights' gradients
+    # a second batch adds to the weights' gradients: the fp32 sum goes on from the first's, so by the bound above
+    # (c terms and the start, magnitudes |start| + T) it is within (c + 1) 2^-23 (|start| + T) of twice the first
     before = layer.grad_w2.clone()
+    dy, off, cnt = torch.zeros_like(saved.y), saved.expert_offsets.tolist(), saved.counts.tolist()
+    moe.moe_unpermute_weight_reduce_bwd(dout, saved.y, saved.inv_perm, tw, dy, torch.empty_like(tw))
     layer.backward(dout, saved)
-    assert torch.allclose(layer.grad_w2, 2 * before, rtol=2.0 ** -20, atol=1e-30)
+    for e, c in enumerate(cnt):
+        r = slice(off[e], off[e] + c)
+        mag = before[e].double().abs() + dy[r].double().abs().T.contiguous() @ saved.act[r].double().abs()
+        err = (layer.grad_w2[e].double() - 2 * before[e].double()).abs()
+        assert (err <= (c + 1) * 2.0 ** -23 * mag).all(), e
     # and the clip scales both to the norm asked for
     norm = float(layer.clip_gradients(0.25))
     total = float((layer.grad_w13.double() ** 2).sum() + (layer.grad_w2.double() ** 2).sum()) ** 0.5

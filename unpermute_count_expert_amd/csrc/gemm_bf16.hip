@@ -5,30 +5,61 @@
 //   dgrad    dx[r,k]  = sum_n dy[r,n] w[e,n,k]          (contraction: n)
 //   wgrad    dw[e,n,k] (+)= sum_{r of e} dy[r,n] a[r,k] (contraction: e's rows)
 //
-// fp32 sums, one rounding to bf16.
+// fp32 sums, one rounding to bf16.  Two kernels:
 //
-// Design:
-//  * One kernel for the three: an output tile of BM x 256 per 512-thread
-//    block (8 waves, 2 x 4, each 16*MI x 64 of it in 16x16x32 MFMAs), the
-//    contraction in steps of 64.  An operand whose contraction index is
-//    contiguous in memory (rows of a or dy; w in the forward) lies in LDS as
-//    128-byte rows and is read 16 bytes a lane; one whose output index is
-//    contiguous (w in dgrad, both in wgrad) lies as it is in memory, one
-//    contraction index a row, and is transposed on the way to the registers
-//    by ds_read_b64_tr_b16.  So no operand is ever transposed in memory.
-//  * Operands move global -> LDS by buffer loads with LDS destination through
-//    a ring of stages.  The buffer descriptor ends at the segment's (or the
-//    matrix's) last byte, so everything past it, ragged rows and the tail of
-//    the contraction included, arrives as zeros without a read: rows past a
-//    segment never meet the sum, whatever they hold, and the per-lane
-//    offsets are the same in every tile.
+// k_tiles, for experts of more than a few rows.
+//  * An output tile of 256 (or 128) x 256 per 512-thread block, one block per
+//    CU, the contraction in steps of 64: eight waves, 2 x 4, each with 128
+//    (64) x 64 of the tile in 16x16x32 MFMAs.
+//  * Operands move global -> LDS by buffer loads with LDS destination, in
+//    granules of 8 KB: 64 output indexes by 64 contraction indexes.  An
+//    operand whose contraction index is contiguous in memory (rows of a or
+//    dy; w in the forward) lies in its granules as 64 rows of 128 bytes and
+//    is read 16 bytes a lane; one whose output index is contiguous (w in
+//    dgrad, both in wgrad) lies as in memory, one contraction index a row,
+//    and is transposed on its way to the registers by ds_read_b64_tr_b16.  So
+//    nothing is ever transposed in memory, and both layouts read without
+//    bank conflicts (counted: none).
+//  * The buffer descriptor of a granule ends with the last byte that belongs
+//    to it, so ragged rows, the tail of the contraction and whole granules
+//    past the tile arrive as zeros without a read; rows past a segment never
+//    meet a sum, whatever they hold, and a lane's offsets are the same in
+//    every tile.
+//  * Two groups of four waves, one of each on every SIMD, run one phase
+//    apart: while one group reads a step's fragments into registers (all of
+//    them, 96 VGPRs) and issues loads, the other multiplies from its
+//    registers; a barrier swaps the roles.  A granule is free as soon as its
+//    readers have it in registers, long before they have multiplied it, so a
+//    ring of 19 granules (152 KB, the LDS but for the tile tables) keeps up
+//    to 104 KB in flight, most of it for three phases.  What was measured on
+//    the way (16384 tokens, top-8, 128 experts, 1536 x 2048, forward): two
+//    whole stages of 64 KB, all waves in step, 0.89 ms; loads alone 0.69 ms,
+//    multiplies alone 0.64 ms.  The ring takes the loads alone to 0.45 ms,
+//    the groups the multiplies alone to 0.55 ms and both together to 0.75 ms
+//    (1100 TFLOP/s).  Past that the clock gives: at 64% of the MFMA rate it
+//    is down to 1.5-1.8 GHz (dgrad and wgrad, at 50%, run at 2.0 GHz).
+//  * Not kept: four waves of 128 x 128 with fragments double-buffered (one
+//    wave per SIMD; 0.96 ms), steps of 32 in four stages (0.96 ms, half-line
+//    reads), a prefetch of later steps into L2 (slower by its own reads: the
+//    loads are bound by their number), raised wave priority around the
+//    multiplies (level), loads issued by the multiplying group as well (0.82
+//    ms: its issue slots are what the MFMAs need).
 //  * The weight-side fragment is the MFMA's first operand, so a lane holds
 //    four consecutive columns of one row; for bf16 two column blocks are
 //    exchanged between neighbouring 16-lane rows (v_permlane16_swap) to 16
-//    bytes a store.
-//  * Persistent grid, tiles dealt to the XCDs in contiguous eighths of the
-//    (expert, m-tile, n-tile) sequence, the operand stream running ahead
-//    across tile boundaries.
+//    bytes a store, through a descriptor that ends with the last valid row.
+//  * Persistent grid; tiles dealt to the XCDs in contiguous eighths of the
+//    (expert, n-tile, m-tile) sequence, m-tiles fastest: an expert's weights
+//    are then read by tiles that run together (n-tiles fastest: forward 1-5%
+//    and weight gradient 5% slower), and the operand stream runs ahead across
+//    tile boundaries.
+//
+// k_few, for a few rows per expert (decoding), where the weights' bytes are
+// the time and 256-column tiles would leave most CUs idle: 16 rows by 32 (64
+// in dgrad) columns per four waves that split the contraction, each wave
+// streaming its own share through its own three LDS stages without barriers,
+// the four sums added in a fixed order.  One token, top-8, 1536 x 2048 (50 MB
+// of weights): 11.9 us against 31 us on k_tiles; 64 tokens 137 against 169.
 #include "moe_device.hpp"
 #include "moe_internal.hpp"
 
@@ -46,7 +77,10 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(3))) const v8bf* lds_v8;
+typedef __attribute__((address_space(3))) v4s* lds_v4;
 
 // rows [lo, hi) of expert e, cut at the next segment and at cap_rows
 __device__ __forceinline__ void segment(const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts,
@@ -60,214 +94,228 @@ __device__ __forceinline__ void segment(const int32_t* __restrict__ offsets, con
     hi = (int)(l + c < end ? l + c : end);
 }
 
-template <int N>
-__device__ __forceinline__ void wait_loads_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+// Exclusive prefix over the experts of nt (two consecutive experts a thread)
+// into pre[0 .. El), and the total, both capped at `most`: disjoint segments
+// never reach the cap, and overlapping ones (offsets out of order) cannot
+// push a sum past it.  wsum: LDS scratch of kWaves values.  All 512 threads
+// call it; it ends with a barrier.
+__device__ __forceinline__ int expert_prefix(const int (&nt)[2], int El, int64_t most, int* pre, int64_t* wsum) {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t sum = (int64_t)nt[0] + nt[1];
+    const int64_t incl = wave_inclusive_scan(sum);
+    if (lane == kWave - 1) wsum[wave] = incl;
+    __syncthreads();
+    int64_t run = incl - sum, total = 0;
+    for (int w = 0; w < kWaves; ++w) {
+        const int64_t v = wsum[w];
+        if (w < wave) run += v;
+        total += v;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int e = threadIdx.x * 2 + j;
+        if (e < El) pre[e] = (int)(run < most ? run : most);
+        run += nt[j];
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane((int)(total < most ? total : most));
 }
 
 // 16 bytes a lane from base + voff to LDS byte lds + 16 * lane; zeros where
-// voff + 16 > bytes
-__device__ __forceinline__ void dma16(const void* base, uint32_t bytes, uint32_t voff, uint32_t lds) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+// they do not lie in the first `bytes` bytes
+__device__ __forceinline__ void dma16(const void* base, int bytes, uint32_t voff, uint32_t lds) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, max(bytes, 0), 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(uintptr_t)lds, 16, (int)voff, 0, 0, 0);
 }
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset past every descriptor: zeros, or not stored
 
-// ---- the two LDS layouts of an operand stage of W output indexes ------------
-// Rows: 128 bytes for each output index, the 16-byte chunk c of row r at
-// position c ^ (r mod 8) ^ (r / 8 mod 2): 16 lanes reading a chunk of 16 rows
-// touch 16 distinct bank groups.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// ---- LDS layouts -------------------------------------------------------------
+// Row layout: 128 bytes for each output index, the 16-byte chunk c of row r at
+// position c ^ (r mod 8) ^ (r / 8 mod 2).  A 128-bit LDS read serves sixteen
+// lanes at a time, half of them from one 16-lane row of the wave and half
+// from the next, so neighbouring lane rows read chunks two apart: lane row g
+// takes chunk 2 g in the first half of a step and 2 g + 1 in the second.
 __device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3) & 1); }
-// Columns: 2 * W bytes for each contraction index k, the 32-byte slot s (16
-// output indexes) at slot s ^ hx(k): the eight contraction rows that half a
-// wave's transposing read touches lie in eight distinct slots.
-__device__ __forceinline__ int hx(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+// Column layout: 128 bytes (64 output indexes) for each contraction index k,
+// the 32-byte slot s at slot s ^ fx(k): the eight contraction rows that half
+// a wave's transposing read touches (k = 16 g + 0..3) lie in eight distinct
+// slots of two adjacent rows.
+__device__ __forceinline__ int fx(int k) { return ((k >> 1) & 1) | (((k >> 4) & 1) << 1); }
 
-// The global byte offset that lane `lane` of the idx-th 1 KB of a stage
-// fetches (ld: bytes between rows in memory).
-template <bool T, int W>
-__device__ __forceinline__ uint32_t dma_offset(int idx, int lane, int ld) {
-    if constexpr (T) {
-        constexpr int RB = 2 * W;
-        const int byte = idx * 1024 + lane * 16;
-        const int k = byte / RB, pos = (byte % RB) >> 4;
-        return (uint32_t)(k * ld + ((((pos >> 1) ^ hx(k)) << 1) | (pos & 1)) * 16);
-    } else {
-        const int r = idx * 8 + (lane >> 3);
-        return (uint32_t)(r * ld + swz(lane & 7, r) * 16);
-    }
+// 16 output indexes by 32 contraction indexes at LDS byte `at` (column
+// layout): contraction rows k..k+3 and k+4..k+7 of the lane's row group
+__device__ __forceinline__ v8bf read_columns(uint32_t at) {
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(uintptr_t)at);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(uintptr_t)(at + 512));
+    return __builtin_bit_cast(v8bf, v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
 }
 
-// A lane's fragment of 16 output indexes (o0 + 16 * b, b the block) by 32
-// contraction indexes (half ks of the stage): base address for block 0 and
-// half 0, then by xor and immediate offsets.
-template <bool T, int W>
-struct Frag {
-    uint32_t base;
-    __device__ __forceinline__ void init(int o0, int lane) {
-        if constexpr (T) {
-            const int k = 8 * (lane >> 4) + ((lane & 15) >> 2);
-            base = (uint32_t)(k * 2 * W + (((o0 >> 4) ^ hx(k)) << 5) + (lane & 3) * 8);
-        } else {
-            const int r = o0 + (lane & 15);
-            base = (uint32_t)(r * 128 + (swz(lane >> 4, r) << 4));
-        }
-    }
-    __device__ __forceinline__ v8bf read(const uint8_t* stage, int b, int ks) const {
-        if constexpr (T) {
-            // (slot ^ hx) ^ b: o0 / 16 is a multiple of the block count, so xor adds b to the slot
-            typedef __attribute__((address_space(3))) v4s* lp;
-            const uint32_t at = (uint32_t)(uintptr_t)stage + (base ^ (uint32_t)(b << 5)) + ks * 32 * 2 * W;
-            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)at);
-            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)(at + 4 * 2 * W));
-            return __builtin_bit_cast(v8bf, v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
-        } else {
-            return *reinterpret_cast<const v8bf*>(stage + (base ^ (uint32_t)(ks << 6)) + b * 2048);
-        }
-    }
-};
+// two 16-column blocks' sums, four consecutive columns a lane in each, as 16
+// bytes of bf16: lane row g then holds columns 16 (g mod 2) + 8 (g / 2) .. + 7
+__device__ __forceinline__ v4u pack_pair(const v4f& x, const v4f& y) {
+    const auto w0 = __builtin_amdgcn_permlane16_swap(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(y[0], y[1]), false, false);
+    const auto w1 = __builtin_amdgcn_permlane16_swap(f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(y[2], y[3]), false, false);
+    return v4u{w0[0], w1[0], w0[1], w1[1]};
+}
 
-// One block's tiles t, t + nslots, ... of the (expert, m-tile, n-tile)
-// sequence, walked without divisions; all fields are wave-uniform.
+// ---- k_tiles -----------------------------------------------------------------
+constexpr int kGran = 8192;   // a granule
+constexpr int kRing = 19;     // granules in the ring
+constexpr int kTab = 2048;    // ints beside it: together the CU's 160 KB
+
+// One block's tiles t, t + nslots, ... ; all fields are wave-uniform.
 struct Cursor {
     int64_t t;
-    int tm, tn, e, lo, hi;
+    int e, lo, hi;   // the tile's expert and its rows
+    int tm, tn;      // the tile's place among the expert's m-tiles and n-tiles
     bool valid;
 };
 
-template <int MODE, int MI, bool F32>
-__global__ __launch_bounds__(kThreads, 1) void k_gemm(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
-                                                      const int32_t* __restrict__ offsets,
-                                                      const int32_t* __restrict__ counts, int El, int64_t cap_rows,
-                                                      int n_out, int k_in, int accumulate, void* __restrict__ out) {
-    constexpr int BM = 32 * MI;
-    constexpr bool AT = MODE == kWgrad, BT = MODE != kFwd;
-    constexpr int kStageA = BM * BK * 2, kStage = kStageA + BN * BK * 2;
-    constexpr int kStages = MI == 8 ? 2 : 3;
-    constexpr int kADma = BM / 64, kBDma = 4;
-    constexpr int kPer = kMaxLocalExperts / kThreads;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[kStages * kStage];
-    __shared__ int s_tpre[kMaxLocalExperts + 1];   // first m-tile of expert e
-    __shared__ int s_lo[kMaxLocalExperts], s_hi[kMaxLocalExperts];
-    __shared__ int s_wsum[kWaves];
+// NA: granules of the row operand per wave group (the tile has 128 * NA rows).
+// A step's granules are numbered p = 0 .. P - 1: group 0's NA of the row
+// operand, four of the weight-side operand (one per wave column), group 1's
+// NA.  Granule p of the block's step i lies in ring slot (P i + p) mod kRing.
+//
+// Phases.  In phase 2 i group 0 reads the fragments of step i (group 1
+// multiplies step i - 1), in phase 2 i + 1 group 1 reads them (group 0
+// multiplies).  Group 0's own NA granules are free after phase 2 i, the other
+// NA + 4 after phase 2 i + 1, and each slot is refilled in the next phase, by
+// the reading group: with R = kRing mod P, group 1 in its phases moves the
+// granules R .. R + NA - 1 of each step, group 0 the others.  The waits count
+// the loads that a wave has issued after the one needed; they are exact,
+// because past the last tile the stream goes on with loads of zero bytes.
+// F32: fp32 outputs; ACC: added to what is there.
+template <int MODE, int NA, bool F32, bool ACC>
+__global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
+                                                       const int32_t* __restrict__ offsets,
+                                                       const int32_t* __restrict__ counts, int El, int64_t cap_rows,
+                                                       int n_out, int k_in, void* __restrict__ out) {
+    constexpr int MI = 4 * NA, BM = 128 * NA, NJ = 4;
+    constexpr bool AT = MODE == kWgrad, BT = MODE != kFwd;   // column layout
+    constexpr int P = 2 * NA + 4, R = kRing % P;
+    constexpr int kAhead = (kRing - NA - 4) / P;   // the step that the first even phase goes on loading
+    static_assert(R <= 4 && (kRing - NA - 4) % P == R + NA, "the phases' shares of a step");
+    // loads (two a granule and wave) issued after the last one needed: group
+    // 0 before even and odd phases, group 1 before even ones (its granules
+    // are all needed there)
+    constexpr int kEven0 = 2 * (NA + R + (kAhead - 1) * (NA + 4)), kOdd0 = 2 * (R + kAhead * (NA + 4));
+    constexpr int kEven1 = 2 * kAhead * NA;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing * kGran];
+    __shared__ int s_tab[kTab];
 
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int N = MODE == kFwd ? n_out : k_in;        // output columns
-    const int ntm_w = (n_out + BM - 1) / BM;          // wgrad: m-tiles of an expert
+    const int grp = wave >> 2, wn = wave & 3;
+    const int N = MODE == kFwd ? n_out : k_in;   // output columns
 
-    int nt[kPer], tsum = 0;
+    // first m-tile of each expert and, where they fit, its rows
+    int* s_tpre = s_tab;
+    const bool rows_in_lds = 3 * El <= kTab;
+    int* s_lo = s_tab + El;
+    int* s_hi = s_lo + El;
+    const int ntm_w = (n_out + BM - 1) / BM;   // wgrad: m-tiles of every expert
+    int nt[2];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = tid * kPer + j;
+    for (int j = 0; j < 2; ++j) {
+        const int e = tid * 2 + j;
         nt[j] = 0;
         if (e < El) {
             int lo, hi;
             segment(offsets, counts, cap_rows, e, lo, hi);
-            s_lo[e] = lo;
-            s_hi[e] = hi;
+            if (rows_in_lds) {
+                s_lo[e] = lo;
+                s_hi[e] = hi;
+            }
             // an expert without rows has a gradient of zeros to write, or nothing to add
-            nt[j] = MODE == kWgrad ? (accumulate && hi == lo ? 0 : ntm_w) : (hi - lo + BM - 1) / BM;
+            nt[j] = MODE == kWgrad ? (ACC && hi == lo ? 0 : ntm_w) : (hi - lo + BM - 1) / BM;
         }
-        tsum += nt[j];
     }
-    const int incl = wave_inclusive_scan(tsum);
-    if (lane == kWave - 1) s_wsum[wave] = incl;
-    __syncthreads();
-    int run = incl - tsum;
-    for (int w = 0; w < wave; ++w) run += s_wsum[w];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = tid * kPer + j;
-        if (e < El) s_tpre[e] = run;
-        run += nt[j];
-    }
-    if (tid == kThreads - 1) s_tpre[El] = run;
-    __syncthreads();
-
-    const int mtiles = __builtin_amdgcn_readfirstlane(s_tpre[El]);
+    const int mtiles = expert_prefix(nt, El, MODE == kWgrad ? (int64_t)El * ntm_w : cap_rows / BM + El, s_tpre,
+                                     reinterpret_cast<int64_t*>(smem));
     const int ntn = (N + BN - 1) / BN;
     const int xcd = blockIdx.x & 7, nslots = gridDim.x >> 3;
-    const int64_t total = (int64_t)mtiles * ntn;
-    const int64_t t_hi = total * (xcd + 1) / 8;
-    const int step_q = nslots / ntn, step_r = nslots - step_q * ntn;
+    const int64_t total = (int64_t)mtiles * ntn, t_hi = total * (xcd + 1) / 8;
 
-    auto fill = [&](Cursor& c) __attribute__((always_inline)) {
-        c.lo = __builtin_amdgcn_readfirstlane(s_lo[c.e]);
-        c.hi = __builtin_amdgcn_readfirstlane(s_hi[c.e]);
+    auto place = [&](Cursor& c) __attribute__((always_inline)) {   // c.t lies in expert c.e
+        const int first = __builtin_amdgcn_readfirstlane(s_tpre[c.e]);
+        const int end = c.e + 1 < El ? __builtin_amdgcn_readfirstlane(s_tpre[c.e + 1]) : mtiles;
+        const uint32_t mt = (uint32_t)(end - first);
+        const uint32_t local = (uint32_t)(c.t - (int64_t)first * ntn);
+        c.tn = (int)(local / mt);
+        c.tm = (int)(local - (uint32_t)c.tn * mt);
+        int lo, hi;
+        if (rows_in_lds) {
+            lo = s_lo[c.e];
+            hi = s_hi[c.e];
+        } else {
+            segment(offsets, counts, cap_rows, c.e, lo, hi);
+        }
+        c.lo = __builtin_amdgcn_readfirstlane(lo);
+        c.hi = __builtin_amdgcn_readfirstlane(hi);
     };
     auto start = [&](Cursor& c) __attribute__((always_inline)) {
         c.t = total * xcd / 8 + (blockIdx.x >> 3);
         c.valid = c.t < t_hi;
         c.tm = c.tn = c.e = c.lo = c.hi = 0;
         if (!c.valid) return;
-        c.tm = (int)(c.t / ntn);
-        c.tn = (int)(c.t - (int64_t)c.tm * ntn);
-        int lo = 0, hi = El - 1;   // the last expert with s_tpre[e] <= tm
+        int lo = 0, hi = El - 1;   // the last expert whose first tile is not after t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (s_tpre[mid] <= c.tm) lo = mid; else hi = mid - 1;
+            if ((int64_t)s_tpre[mid] * ntn <= c.t) lo = mid; else hi = mid - 1;
         }
         c.e = __builtin_amdgcn_readfirstlane(lo);
-        fill(c);
+        place(c);
     };
     auto next = [&](Cursor& c) __attribute__((always_inline)) {
         c.t += nslots;
         c.valid = c.t < t_hi;
         if (!c.valid) return;
-        c.tn += step_r;
-        c.tm += step_q;
-        if (c.tn >= ntn) {
-            c.tn -= ntn;
-            ++c.tm;
-        }
-        bool moved = false;
-        while (c.e + 1 < El && s_tpre[c.e + 1] <= c.tm) {
-            ++c.e;
-            moved = true;
-        }
+        while (c.e + 1 < El && (int64_t)s_tpre[c.e + 1] * ntn <= c.t) ++c.e;
         c.e = __builtin_amdgcn_readfirstlane(c.e);
-        if (moved) fill(c);
+        place(c);
     };
-    // first output row of a tile (a row of the buffer; wgrad: a weight row),
-    // the end of its valid rows, and its contraction length
+    // a tile's first output row (a row of the buffer; wgrad: of the expert's
+    // weights) and its contraction's length
     auto m_first = [&](const Cursor& c) __attribute__((always_inline)) {
-        const int m = (c.tm - __builtin_amdgcn_readfirstlane(s_tpre[c.e])) * BM;
-        return MODE == kWgrad ? m : c.lo + m;
+        return MODE == kWgrad ? c.tm * BM : c.lo + c.tm * BM;
     };
     auto depth = [&](const Cursor& c) __attribute__((always_inline)) {
         return MODE == kFwd ? k_in : MODE == kDgrad ? n_out : c.hi - c.lo;
     };
 
-    // ---- the operand stream --------------------------------------------------
-    const int ldA = 2 * (MODE == kFwd ? k_in : n_out), ldB = 2 * k_in;   // bytes
-    uint32_t voA[kADma], voB[kBDma];
-    int cA[kADma], cB[kBDma];   // row layout: the 16-byte chunk, masked past the contraction's end
-#pragma unroll
-    for (int j = 0; j < kADma; ++j) {
-        const int idx = wave * kADma + j;
-        voA[j] = dma_offset<AT, BM>(idx, lane, ldA);
-        cA[j] = swz(lane & 7, idx * 8 + (lane >> 3)) * 8;
-    }
-#pragma unroll
-    for (int j = 0; j < kBDma; ++j) {
-        const int idx = wave * kBDma + j;
-        voB[j] = dma_offset<BT, BN>(idx, lane, ldB);
-        cB[j] = swz(lane & 7, idx * 8 + (lane >> 3)) * 8;
-    }
+    // ---- the operand stream -------------------------------------------------
+    const int ldA = 2 * (MODE == kFwd ? k_in : n_out), ldB = 2 * k_in;   // bytes between rows in memory
+    // A granule is eight kilobytes of eight rows; wave wn of a group moves
+    // kilobytes 2 wn and 2 wn + 1, whose rows lie 8 * ld apart (and whose row
+    // layout swaps neighbouring chunks).
+    const int gr = wn * 16 + (lane >> 3);
+    const int crow = swz(lane & 7, gr), ccol = ((((lane & 7) >> 1) ^ fx(gr)) << 1) | (lane & 1);
+    const uint32_t voA = (uint32_t)(gr * ldA + (AT ? ccol : crow) * 16);
+    const uint32_t voB = MODE == kFwd ? voA : (uint32_t)(gr * ldB + (BT ? ccol : crow) * 16);
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     Cursor d;
     start(d);
-    const uint8_t *dA = nullptr, *dB = nullptr;
-    int d_left = 0, d_slot = 0;
-    int d_mrows = 0, d_ncols = 0;   // output rows and columns from the tile's origin on
-    int pending = 0;                // steps issued and not yet consumed
+    if (!d.valid) return;   // no tile for this block
+    const uint8_t *dA, *dB;   // the step's operands
+    int d_left, tA, tB;       // contraction left; operand bytes that do not depend on the step
+    int d_q = 0;              // ring slot of the step's granule 0
+    const int gA = AT ? 128 : 64 * ldA, gB = BT ? 128 : 64 * ldB;   // bytes between granules in memory
     auto d_tile = [&]() __attribute__((always_inline)) {
         const int m0 = m_first(d), n0 = d.tn * BN;
         d_left = depth(d);
-        d_mrows = (MODE == kWgrad ? n_out : d.hi) - m0;
-        d_ncols = N - n0;
+        const int mrows = min((MODE == kWgrad ? n_out : d.hi) - m0, BM), ncols = min(N - n0, BN);
+        tA = AT ? mrows * 2 : (mrows - 1) * ldA;
+        tB = BT ? ncols * 2 : (ncols - 1) * ldB;
         const uint8_t* A = reinterpret_cast<const uint8_t*>(a);
         const uint8_t* B = reinterpret_cast<const uint8_t*>(b);
         dA = MODE == kWgrad ? A + (int64_t)d.lo * ldA + m0 * 2 : A + (int64_t)m0 * ldA;
@@ -275,140 +323,414 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm(const uint16_t* __restrict
            : MODE == kDgrad ? B + (int64_t)d.e * n_out * ldB + n0 * 2
                             : B + (int64_t)d.lo * ldB + n0 * 2;
     };
-    if (d.valid) d_tile();
-    auto issue = [&]() __attribute__((always_inline)) {
-        const int kk = d_left < BK ? d_left : BK;
-        // bytes from the base that belong to the operand; a row layout's rows
-        // all lie inside it, a column layout's last row ends with its width
-        const uint32_t bytesA = AT ? (kk > 0 ? (uint32_t)((kk - 1) * ldA + d_mrows * 2) : 0u)
-                                   : (uint32_t)(((d_mrows < BM ? d_mrows : BM) - 1) * ldA + d_left * 2);
-        const uint32_t bytesB = BT ? (kk > 0 ? (uint32_t)((kk - 1) * ldB + d_ncols * 2) : 0u)
-                                   : (uint32_t)(((d_ncols < BN ? d_ncols : BN) - 1) * ldB + d_left * 2);
-        const uint32_t at = lds0 + d_slot * kStage;
-        const bool tail = d_left < BK;
+    d_tile();
+    auto put = [&](int p) __attribute__((always_inline)) {   // granule p of the step
+        const bool isA = p < NA || p >= NA + 4;
+        const int g = p < NA ? p : isA ? p - 4 : p - NA;
+        const bool T = isA ? AT : BT;
+        const int ld = isA ? ldA : ldB, go = g * (isA ? gA : gB);
+        // from the step's first byte to the last one that belongs to it
+        const int bytes = T ? (min(d_left, BK) - 1) * ld + (isA ? tA : tB) : d_left * 2 + (isA ? tA : tB);
+        const int q = d_q + p >= kRing ? d_q + p - kRing : d_q + p;
 #pragma unroll
-        for (int j = 0; j < kADma; ++j) {
-            uint32_t v = voA[j];
-            if (!AT && tail) v |= cA[j] >= d_left ? 0x80000000u : 0u;   // past any descriptor: zeros
-            dma16(dA, bytesA, v, at + (wave * kADma + j) * 1024);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v = (isA ? voA : voB) + (T || h == 0 ? 0 : 16 - ((crow & 1) << 5));
+            if (!T && d_left < BK)   // the contraction's tail: the chunks past it read as zeros
+                v |= (crow ^ h) * 8 >= d_left ? kNowhere : 0u;
+            const int at = go + h * 8 * ld;
+            dma16((isA ? dA : dB) + at, bytes - at, v, lds0 + q * kGran + wn * 2048 + h * 1024);
         }
-#pragma unroll
-        for (int j = 0; j < kBDma; ++j) {
-            uint32_t v = voB[j];
-            if (!BT && tail) v |= cB[j] >= d_left ? 0x80000000u : 0u;
-            dma16(dB, bytesB, v, at + kStageA + (wave * kBDma + j) * 1024);
-        }
+    };
+    auto advance = [&]() __attribute__((always_inline)) {
         dA += AT ? (int64_t)BK * ldA : BK * 2;
         dB += BT ? (int64_t)BK * ldB : BK * 2;
         d_left -= BK;
-        d_slot = d_slot + 1 == kStages ? 0 : d_slot + 1;
-        ++pending;
+        d_q = d_q + P >= kRing ? d_q + P - kRing : d_q + P;
         if (d_left <= 0) {
-            next(d);
-            if (d.valid) d_tile();
+            if (d.valid) next(d);
+            if (d.valid) {
+                d_tile();
+            } else {   // past the last tile: zero bytes
+                d_left = 0;
+                tA = tB = -(1 << 30);
+            }
+        }
+    };
+    auto even_puts = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = R + NA; p < P; ++p) put(p);
+        advance();
+#pragma unroll
+        for (int p = 0; p < R; ++p) put(p);
+    };
+    auto odd_puts = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = R; p < R + NA; ++p) put(p);
+        advance();
+    };
+    // the ring but for what the first even phase loads
+    if (grp == 0) {
+#pragma unroll
+        for (int q = 0; q < kRing - NA - 4; ++q) {
+            if (q % P < R || q % P >= R + NA) put(q % P);
+            if (q % P == P - 1) advance();
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q <= kAhead; ++q) odd_puts();
+    }
+
+    // ---- the compute side ---------------------------------------------------
+    const int kc = 16 * (lane >> 4) + ((lane & 15) >> 2);   // column layout: the lane's contraction row
+    const uint32_t col = (uint32_t)(kc * 128 + (fx(kc) << 5) + (lane & 3) * 8);
+    const uint32_t row = (uint32_t)((lane & 15) * 128 + (swz(2 * (lane >> 4), lane & 15) << 4));
+    const uint32_t rA = AT ? col : row, rB = BT ? col : row;   // the lane's byte in a granule
+    int c_q = 0;   // ring slot of the step's granule 0
+    auto granule = [&](int p) __attribute__((always_inline)) {
+        return lds0 + (c_q + p >= kRing ? c_q + p - kRing : c_q + p) * kGran;
+    };
+    // block blk (16 output indexes) and half ks of a granule's contraction
+    auto frag = [&](bool T, uint32_t at, int blk, int ks) __attribute__((always_inline)) {
+        return T ? read_columns((at ^ (uint32_t)(blk << 5)) + ks * 1024)
+                 : *(lds_v8)(uintptr_t)((at ^ (uint32_t)(ks << 4)) + blk * 2048);
+    };
+    v4f acc[MI][NJ];
+    auto load = [&](v8bf (&fa)[2][MI], v8bf (&fb)[2][NJ]) __attribute__((always_inline)) {
+        const uint32_t bB = granule(NA + wn) + rB;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) fb[ks][j] = frag(BT, bB, j, ks);
+#pragma unroll
+            for (int g = 0; g < NA; ++g) {
+                const uint32_t bA = granule((grp ? NA + 4 : 0) + g) + rA;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fa[ks][4 * g + i] = frag(AT, bA, i, ks);
+            }
+        }
+    };
+    auto multiply = [&](const v8bf (&fa)[2][MI], const v8bf (&fb)[2][NJ]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[ks][j], fa[ks][i], acc[i][j], 0, 0, 0);
+    };
+    // This wave's part of a tile.
+    struct Part {
+        int m0, m_end, n0, e;
+        bool mine;   // any of it is valid
+    } done = {0, 0, 0, 0, false};
+    auto part_of = [&](const Cursor& c) __attribute__((always_inline)) {
+        Part t;
+        t.m0 = m_first(c) + grp * 64 * NA;
+        t.m_end = MODE == kWgrad ? n_out : c.hi;
+        t.n0 = c.tn * BN + wn * 64;
+        t.e = c.e;
+        t.mine = t.m0 < t.m_end && t.n0 < N;
+        return t;
+    };
+    // Its outputs, 16 rows at a time, through a descriptor that ends with the
+    // last valid row; columns past the width go nowhere.
+    constexpr int ES = F32 ? 4 : 2, kPieces = F32 ? NJ : NJ / 2;
+    auto outputs = [&](const Part& t, auto each) __attribute__((always_inline)) {
+        constexpr int kCols = F32 ? 16 : 32;   // between a row's pieces
+        const int g = lane >> 4;
+        const int64_t row0 = MODE == kWgrad ? (int64_t)t.e * n_out + t.m0 : t.m0;
+        uint8_t* o = static_cast<uint8_t*>(out) + (row0 * N + t.n0) * ES;
+        const int w = N - t.n0;   // columns from n0 on
+        const int bytes = ((min(t.m_end - t.m0, 16 * MI) - 1) * N + w) * ES;
+        const int c0 = F32 ? 4 * g : 16 * (g & 1) + 8 * (g >> 1);
+        const uint32_t v = (uint32_t)(((lane & 15) * N + c0) * ES);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                o + (int64_t)i * 16 * N * ES, 0, max(bytes - i * 16 * N * ES, 0), 0x00020000);
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) each(i, p, r, c0 + kCols * p < w ? v + kCols * ES * p : kNowhere);
+            sched_fence();
+        }
+    };
+    auto store = [&]() __attribute__((always_inline)) {
+        if (!done.mine) return;
+        outputs(done, [&](int i, int p, __amdgpu_buffer_rsrc_t r, uint32_t v) __attribute__((always_inline)) {
+            if constexpr (F32)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i][p]), r, v, 0, 0);
+            else   // non-temporal: the next kernel reads it back from HBM
+                __builtin_amdgcn_raw_buffer_store_b128(pack_pair(acc[i][2 * p], acc[i][2 * p + 1]), r, v, 0, 2);
+        });
+    };
+    // The sums' start: zero, or what is there (ACC).  Adding it at the end
+    // instead would save the sums' roundings at its magnitude (2^-24 of it a
+    // step) but needs registers that the fragments hold.
+    auto begin = [&](const Part& t) __attribute__((always_inline)) {
+        if constexpr (ACC) {
+            if (t.mine)
+                outputs(t, [&](int i, int p, __amdgpu_buffer_rsrc_t r, uint32_t v) __attribute__((always_inline)) {
+                    acc[i][p] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, v, 0, 0));
+                });
+        } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         }
     };
 
-    const int wm = wave >> 2, wn = wave & 3;
-    Frag<AT, BM> fA;
-    Frag<BT, BN> fB;
-    fA.init(wm * 16 * MI, lane);
-    fB.init(wn * 64, lane);
-
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
-        if (d.valid) issue();
-
+    // Before a group's reading phase, and before its multiplying phase: the
+    // loads whose data the coming phase reads, whoever reads it, then the
+    // barrier that publishes every wave's.
+    auto to_read = [&]() __attribute__((always_inline)) {
+        sched_fence();
+        if (grp == 0) wait_loads<kEven0>();
+        else wait_loads<63>();   // nothing of group 1's: LDS reads only
+        barrier();
+        sched_fence();
+    };
+    auto to_multiply = [&]() __attribute__((always_inline)) {
+        sched_fence();
+        if (grp == 0) wait_loads<kOdd0>();
+        else wait_loads<kEven1>();
+        barrier();
+        sched_fence();
+    };
     Cursor c;
     start(c);
-    int slot = 0;
+    bool have = false;             // a finished tile's sums are in registers
+    if (grp != 0) to_multiply();   // group 1 runs one phase behind
     while (c.valid) {
-        const int m0 = m_first(c) + wm * 16 * MI;
-        const int m_end = MODE == kWgrad ? n_out : c.hi;
-        const int n0 = c.tn * BN + wn * 64;
-        const bool mine = m0 < m_end && n0 < N;   // else nothing of this wave's part is stored
-        v4f acc[MI][4];
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        const Part t = part_of(c);
         int left = depth(c);
-        do {
-            if (kStages == 2 || pending < 2) wait_loads_barrier<0>();
-            else wait_loads_barrier<kADma + kBDma>();
-            if (d.valid) issue();
-            --pending;
-            if (mine) {
-                const uint8_t* st = smem + slot * kStage;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    v8bf bf[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) bf[j] = fB.read(st + kStageA, j, ks);
-#pragma unroll
-                    for (int i = 0; i < MI; ++i) {
-                        const v8bf af = fA.read(st, i, ks);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af, acc[i][j], 0, 0, 0);
-                    }
-                }
+        bool first = true;
+        do {   // an expert without rows: one step, of zeros
+            to_read();
+            if (first) {
+                if (have) store();
+                sched_fence();
+                done = t;
+                begin(t);
+                first = false;
+                have = true;
             }
-            slot = slot + 1 == kStages ? 0 : slot + 1;
+            v8bf fa[2][MI], fb[2][NJ];   // the step's fragments: dead between steps, where the stores need registers
+            if (t.mine) load(fa, fb);
+            if (grp == 0) even_puts();
+            else odd_puts();
+            c_q = c_q + P >= kRing ? c_q + P - kRing : c_q + P;
+            to_multiply();
+            if (t.mine) multiply(fa, fb);
             left -= BK;
         } while (left > 0);
-
-        if (mine) {
-            const int g = lane >> 4;
-            const int64_t row0 = MODE == kWgrad ? (int64_t)c.e * n_out + m0 : m0;
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int r = 16 * i + (lane & 15);
-                const bool ok = m0 + r < m_end;
-                if constexpr (F32) {
-                    float* o = static_cast<float*>(out) + (row0 + r) * N;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int col = n0 + 16 * j + 4 * g;
-                        if (ok && col < N) {
-                            v4f v = acc[i][j];
-                            if (accumulate) v += *reinterpret_cast<const v4f*>(o + col);
-                            *reinterpret_cast<v4f*>(o + col) = v;
-                        }
-                    }
-                } else {
-                    uint16_t* o = static_cast<uint16_t*>(out) + (row0 + r) * N;
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const v4f x = acc[i][2 * p], y = acc[i][2 * p + 1];
-                        const auto w0 = __builtin_amdgcn_permlane16_swap(f32x2_to_bf16x2(x[0], x[1]),
-                                                                         f32x2_to_bf16x2(y[0], y[1]), false, false);
-                        const auto w1 = __builtin_amdgcn_permlane16_swap(f32x2_to_bf16x2(x[2], x[3]),
-                                                                         f32x2_to_bf16x2(y[2], y[3]), false, false);
-                        const int col = n0 + 32 * p + 16 * (g & 1) + 8 * (g >> 1);
-                        if (ok && col < N) store_once16(o + col, uint4{w0[0], w1[0], w0[1], w1[1]});
-                    }
-                }
-            }
-        }
         next(c);
     }
+    if (grp == 0) to_read();   // as many barriers as group 1
+    if (have) store();
+    wait_loads<0>();   // no load may still write this block's LDS when it ends
 }
 
-template <int MODE, bool F32>
+// ---- k_few -------------------------------------------------------------------
+constexpr int kFewStages = 3;
+
+// A unit: 16 rows of an expert by NC columns.  A block works on two units at a
+// time, four waves each; wave kw of a unit takes its steps kw, kw + 4, ...
+// (KS of the contraction each: 4 KB of weights and the rows' part).  MODE:
+// forward (row layouts, 32 columns) or dgrad (weights in column layout, 64
+// columns, so that a step still reads whole 128-byte lines).
+template <int MODE>
+__global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
+                                                     const int32_t* __restrict__ offsets,
+                                                     const int32_t* __restrict__ counts, int El, int64_t cap_rows,
+                                                     int n_out, int k_in, uint16_t* __restrict__ out) {
+    static_assert(MODE == kFwd || MODE == kDgrad, "the contraction is not the ragged axis");
+    constexpr bool BT = MODE == kDgrad;
+    constexpr int NC = BT ? 64 : 32, KS = BT ? 32 : 64;
+    constexpr int NJ = NC / 16, KK = KS / 32;
+    constexpr int kW = 4096, kStep = kW + 16 * KS * 2;        // a stage: weights, rows
+    constexpr int kADma = 16 * KS * 2 / 1024, kDma = 4 + kADma;   // loads a step
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[kWaves * kFewStages * kStep];
+    __shared__ __attribute__((aligned(16))) float s_red[2][3][16 * NC];
+    __shared__ int s_tpre[kMaxLocalExperts];   // first 16-row tile of each expert
+    const int tid = threadIdx.x;
+    const int lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int uw = wave >> 2, kw = wave & 3;
+    const int N = MODE == kFwd ? n_out : k_in, C = MODE == kFwd ? k_in : n_out;
+    int nt[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int e = tid * 2 + j;
+        nt[j] = 0;
+        if (e < El) {
+            int lo, hi;
+            segment(offsets, counts, cap_rows, e, lo, hi);
+            nt[j] = (hi - lo + 15) / 16;
+        }
+    }
+    const int tiles = expert_prefix(nt, El, cap_rows / 16 + El, s_tpre, reinterpret_cast<int64_t*>(smem));
+    const int ncu = (N + NC - 1) / NC;
+    const int64_t units = (int64_t)tiles * ncu;
+    const int64_t first = 2 * (int64_t)blockIdx.x, stride = 2 * (int64_t)gridDim.x;
+    if (first >= units) return;
+    const int S = (C + KS - 1) / KS;
+    const int steps = (S - kw + 3) / 4;   // this wave's steps of every unit; may be none
+
+    struct Unit {
+        int e, m0, rows, n0;   // rows 0: past the last unit
+    };
+    auto unit_of = [&](int64_t u) __attribute__((always_inline)) {
+        Unit x = {0, 0, 0, 0};
+        if (u >= units) return x;
+        const int t = (int)(u / ncu);
+        x.n0 = (int)(u - (int64_t)t * ncu) * NC;
+        int at = 0;   // experts whose first tile is not after t
+        for (int j = 0; j < El; j += kWave)
+            at += __popcll(ballot(j + lane < El && s_tpre[min(j + lane, El - 1)] <= t));
+        x.e = __builtin_amdgcn_readfirstlane(at - 1);
+        int lo, hi;
+        segment(offsets, counts, cap_rows, x.e, lo, hi);
+        x.m0 = __builtin_amdgcn_readfirstlane(lo + 16 * (t - s_tpre[x.e]));
+        x.rows = min(16, __builtin_amdgcn_readfirstlane(hi) - x.m0);
+        return x;
+    };
+
+    // the operand stream of this wave: weights in kilobytes of eight rows
+    // (columns of the output, or contraction indexes), then the rows
+    const int ldA = 2 * C, ldB = 2 * k_in;
+    const int rw = lane >> 3;
+    const int cB = BT ? ((((lane & 7) >> 1) ^ ((rw >> 1) & 1)) << 1) | (lane & 1) : swz(lane & 7, rw);
+    const uint32_t voB = (uint32_t)(rw * ldB + cB * 16);
+    const int ra = BT ? lane >> 2 : lane >> 3;
+    const int cA = BT ? (lane & 3) ^ ((ra >> 2) & 3) : swz(lane & 7, ra);
+    const uint32_t voA = (uint32_t)(ra * ldA + cA * 16);
+    const uint32_t ring = (uint32_t)(uintptr_t)smem + wave * kFewStages * kStep;
+    int64_t d_u = first + uw;
+    Unit d = unit_of(d_u);
+    int d_j = 0, d_slot = 0;
+    auto issue = [&]() __attribute__((always_inline)) {
+        const int k0 = (kw + 4 * d_j) * KS, left = d.rows > 0 ? C - k0 : 0;
+        const uint32_t at = ring + d_slot * kStep;
+        const uint8_t* W = reinterpret_cast<const uint8_t*>(b) + (int64_t)d.e * n_out * ldB +
+                           (BT ? (int64_t)k0 * ldB + d.n0 * 2 : (int64_t)d.n0 * ldB + k0 * 2);
+        const int wb = left <= 0 ? 0 : BT ? (min(left, KS) - 1) * ldB + (N - d.n0) * 2
+                                          : (min(N - d.n0, NC) - 1) * ldB + left * 2;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            // the next eight rows swap neighbouring chunks (row layout) or pairs of slots (column layout)
+            uint32_t v = voB + ((h & 1) == 0 ? 0 : BT ? 64 - ((cB & 4) << 5) : 16 - ((cB & 1) << 5));
+            if (!BT && left < KS) v |= (cB ^ (h & 1)) * 8 >= left ? kNowhere : 0u;
+            dma16(W + h * 8 * ldB, wb - h * 8 * ldB, v, at + h * 1024);
+        }
+        const uint8_t* A = reinterpret_cast<const uint8_t*>(a) + (int64_t)d.m0 * ldA + k0 * 2;
+        const int ab = left <= 0 ? 0 : (d.rows - 1) * ldA + left * 2;
+#pragma unroll
+        for (int h = 0; h < kADma; ++h) {
+            uint32_t v = voA + (h == 0 ? 0 : 16 - ((cA & 1) << 5));
+            if (left < KS) v |= (cA ^ h) * 8 >= left ? kNowhere : 0u;
+            dma16(A + h * 8 * ldA, ab - h * 8 * ldA, v, at + kW + h * 1024);
+        }
+        d_slot = d_slot + 1 == kFewStages ? 0 : d_slot + 1;
+        if (++d_j >= steps) {
+            d_j = 0;
+            d_u += stride;
+            d = unit_of(d_u);
+        }
+    };
+    if (steps > 0) {
+#pragma unroll
+        for (int s = 0; s < kFewStages; ++s) issue();
+    }
+
+    const int g = lane >> 4;
+    const int kc = 8 * g + ((lane & 15) >> 2);   // column layout: the lane's contraction row
+    const uint32_t rB = BT ? (uint32_t)(kc * 128 + ((((kc >> 1) & 1) | ((kc >> 3) & 1) << 1) << 5) + (lane & 3) * 8)
+                           : (uint32_t)((lane & 15) * 128 + (swz(2 * g, lane & 15) << 4));
+    const uint32_t rA = BT ? (uint32_t)((lane & 15) * 64 + ((g ^ (((lane & 15) >> 2) & 3)) << 4))
+                           : (uint32_t)((lane & 15) * 128 + (swz(2 * g, lane & 15) << 4));
+    int slot = 0;
+    for (int64_t u = first + uw; u - uw < units; u += stride) {
+        v4f acc[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < steps; ++s) {
+            sched_fence();
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kDma * (kFewStages - 1)) : "memory");   // this step's loads
+            sched_fence();
+            const uint32_t at = ring + slot * kStep;
+            v8bf fa[KK], fb[KK][NJ];
+#pragma unroll
+            for (int ks = 0; ks < KK; ++ks) {
+                fa[ks] = *(lds_v8)(uintptr_t)(at + kW + (rA ^ (uint32_t)(ks << 4)));
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    fb[ks][j] = BT ? read_columns(at + (rB ^ (uint32_t)(j << 5)))
+                                   : *(lds_v8)(uintptr_t)(at + (rB ^ (uint32_t)(ks << 4)) + j * 2048);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is in registers: refill it
+            sched_fence();
+            issue();
+#pragma unroll
+            for (int ks = 0; ks < KK; ++ks)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[ks][j], fa[ks], acc[j], 0, 0, 0);
+            slot = slot + 1 == kFewStages ? 0 : slot + 1;
+        }
+        if (kw > 0) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(&s_red[uw][kw - 1][(j * kWave + lane) * 4]) = acc[j];
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kw == 0) {
+            const Unit x = unit_of(u);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int w = 0; w < 3; ++w)
+                    acc[j] += *reinterpret_cast<const v4f*>(&s_red[uw][w][(j * kWave + lane) * 4]);
+            const int w = N - x.n0;   // columns from n0 on
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                out + (int64_t)x.m0 * N + x.n0, 0, x.rows > 0 ? ((x.rows - 1) * N + w) * 2 : 0, 0x00020000);
+#pragma unroll
+            for (int p = 0; p < NJ / 2; ++p) {
+                const int c = 32 * p + 16 * (g & 1) + 8 * (g >> 1);
+                const uint32_t v = c < w ? (uint32_t)(((lane & 15) * N + c) * 2) : kNowhere;
+                __builtin_amdgcn_raw_buffer_store_b128(pack_pair(acc[2 * p], acc[2 * p + 1]), r, v, 0, 0);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // s_red may be written again
+    }
+    wait_loads<0>();   // no load may still write this block's LDS when it ends
+}
+
+// Which kernel, by the rows expected per expert, r = rows_hint / El.  Measured
+// on 128 experts, top-8, 1536 x 2048 (forward / dgrad, us; k_few, k_tiles of
+// 128 rows, of 256 rows):
+//   r 4   137 / 147   169 / 138   177 / 143
+//   r 8   139 / 152   180 / 139   190 / 142      (768 x 2048, r 8: 78 / 75   76 / 90   80 / 95)
+//   r 16  156 / 183   156 / 142   159 / 143
+//   r 32  217 / 252   184 / 139   193 / 144
+//   r 96  470 / 520   198 / 155   200 / 165
+//   r 128 605 / 718   220 / 225   215 / 184
+// and on 8 experts of 4096 x 4096: r 2 47 / 43, 66 / 68; r 8 52 / 54, 72 / 74;
+// r 32 64 / 75, 59 / 60.  So k_few up to 8 rows, 128-row tiles below 104,
+// 256-row tiles from there on, whatever the direction.  The gradient by the
+// weights has whole matrices as output tiles and takes 256-row tiles always.
+template <int MODE, bool F32, bool ACC>
 hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
-                  int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, int acc, void* out, int num_cus,
-                  hipStream_t s) {
-    const unsigned grid = (unsigned)((num_cus + 7) / 8 * 8);   // whole rounds over the eight XCDs
-    auto go = [&](auto* kern) {
-        kern<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, acc, out);
+                  int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, void* out, int num_cus, hipStream_t s) {
+    const unsigned grid = (unsigned)((num_cus + 7) / 8 * 8);   // the same number of blocks on each of the eight XCDs
+    auto tiles = [&](auto* kernel) {
+        kernel<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, out);
     };
     if constexpr (MODE == kWgrad) {
-        go(k_gemm<MODE, 8, F32>);
+        tiles(k_tiles<MODE, 2, F32, ACC>);
     } else {
-        if (rows_hint >= (int64_t)104 * El) go(k_gemm<MODE, 8, F32>);
-        else if (rows_hint >= (int64_t)48 * El) go(k_gemm<MODE, 4, F32>);
-        else go(k_gemm<MODE, 2, F32>);
+        if (rows_hint >= (int64_t)104 * El) tiles(k_tiles<MODE, 2, F32, ACC>);
+        else if (rows_hint > (int64_t)8 * El) tiles(k_tiles<MODE, 1, F32, ACC>);
+        else k_few<MODE><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
+                                                    static_cast<uint16_t*>(out));
     }
     return hipGetLastError();
 }
@@ -418,20 +740,18 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
 hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* offsets, const int32_t* counts,
                             int El, int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, uint16_t* out,
                             int num_cus, hipStream_t s) {
-    return launch<kFwd, false>(a, w, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, 0, out, num_cus, s);
+    return launch<kFwd, false, false>(a, w, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, out, num_cus, s);
 }
 hipError_t launch_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int32_t* offsets,
                                   const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
                                   int64_t rows_hint, uint16_t* dx, int num_cus, hipStream_t s) {
-    return launch<kDgrad, false>(dy, w, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, 0, dx, num_cus, s);
+    return launch<kDgrad, false, false>(dy, w, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, dx, num_cus, s);
 }
 hipError_t launch_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* offsets,
                                   const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
                                   int64_t rows_hint, bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s) {
-    if (f32)
-        return launch<kWgrad, true>(dy, a, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, accumulate, dw,
-                                    num_cus, s);
-    return launch<kWgrad, false>(dy, a, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, 0, dw, num_cus, s);
+    auto* go = !f32 ? launch<kWgrad, false, false> : accumulate ? launch<kWgrad, true, true> : launch<kWgrad, true, false>;
+    return go(dy, a, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, dw, num_cus, s);
 }
 
 }  // namespace moe
