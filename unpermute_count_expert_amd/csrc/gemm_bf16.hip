@@ -128,6 +128,7 @@ __device__ __forceinline__ void dma16(const void* base, int bytes, uint32_t voff
         __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, max(bytes, 0), 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(uintptr_t)lds, 16, (int)voff, 0, 0, 0);
 }
+constexpr int kNonTemporal = 2;              // the buffer instructions' cache bits
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset past every descriptor: zeros, or not stored
 
 template <int N>
@@ -432,45 +433,82 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         t.mine = t.m0 < t.m_end && t.n0 < N;
         return t;
     };
-    // Its outputs, 16 rows at a time, through a descriptor that ends with the
-    // last valid row; columns past the width go nowhere.
-    constexpr int ES = F32 ? 4 : 2, kPieces = F32 ? NJ : NJ / 2;
-    auto outputs = [&](const Part& t, auto each) __attribute__((always_inline)) {
-        constexpr int kCols = F32 ? 16 : 32;   // between a row's pieces
-        const int g = lane >> 4;
-        const int64_t row0 = MODE == kWgrad ? (int64_t)t.e * n_out + t.m0 : t.m0;
-        uint8_t* o = static_cast<uint8_t*>(out) + (row0 * N + t.n0) * ES;
-        const int w = N - t.n0;   // columns from n0 on
-        const int bytes = ((min(t.m_end - t.m0, 16 * MI) - 1) * N + w) * ES;
-        const int c0 = F32 ? 4 * g : 16 * (g & 1) + 8 * (g >> 1);
-        const uint32_t v = (uint32_t)(((lane & 15) * N + c0) * ES);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                o + (int64_t)i * 16 * N * ES, 0, max(bytes - i * 16 * N * ES, 0), 0x00020000);
-#pragma unroll
-            for (int p = 0; p < kPieces; ++p) each(i, p, r, c0 + kCols * p < w ? v + kCols * ES * p : kNowhere);
-            sched_fence();
-        }
+    // Its outputs, `rows` rows at a time, each time through a descriptor that
+    // ends with the last valid row; columns past the width go nowhere.
+    constexpr int ES = F32 ? 4 : 2, kPieces = F32 ? NJ : NJ / 2, kCols = F32 ? 16 : 32;   // 64-byte pieces of a row
+    const int g = lane >> 4, c0 = F32 ? 4 * g : 16 * (g & 1) + 8 * (g >> 1);
+    struct Rows {
+        uint8_t* o;
+        int w, bytes;   // columns from n0 on, bytes to the end of the last valid row
     };
+    auto rows_of = [&](const Part& t) __attribute__((always_inline)) {
+        const int64_t row0 = MODE == kWgrad ? (int64_t)t.e * n_out + t.m0 : t.m0;
+        Rows x;
+        x.o = static_cast<uint8_t*>(out) + (row0 * N + t.n0) * ES;
+        x.w = N - t.n0;
+        x.bytes = ((min(t.m_end - t.m0, 16 * MI) - 1) * N + x.w) * ES;
+        return x;
+    };
+    auto from_row = [&](const Rows& x, int r) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc(x.o + (int64_t)r * N * ES, 0, max(x.bytes - r * N * ES, 0), 0x00020000);
+    };
+    // Non-temporal stores: what is written is read again from HBM, and a
+    // gradient's bytes are most of a short batch's time.  There (kLines) the
+    // lanes eight apart trade halves of two neighbouring pieces, so that a
+    // store writes eight rows of whole 128-byte lines instead of sixteen of
+    // half lines (512 tokens, 1536 x 2048: fp32 gradients 290 -> 245 us, bf16
+    // 234 -> 149; forward and dgrad are level or 3% slower with it).
     auto store = [&]() __attribute__((always_inline)) {
         if (!done.mine) return;
-        outputs(done, [&](int i, int p, __amdgpu_buffer_rsrc_t r, uint32_t v) __attribute__((always_inline)) {
-            if constexpr (F32)
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i][p]), r, v, 0, 0);
-            else   // non-temporal: the next kernel reads it back from HBM
-                __builtin_amdgcn_raw_buffer_store_b128(pack_pair(acc[i][2 * p], acc[i][2 * p + 1]), r, v, 0, 2);
-        });
+        constexpr bool kLines = MODE == kWgrad;
+        const Rows x = rows_of(done);
+        const bool up = kLines && (lane & 8);
+        const int c1 = c0 + (up ? kCols : 0);
+        const uint32_t v = (uint32_t)(((lane & (kLines ? 7 : 15)) * N + c1) * ES);
+        auto at = [&](int p) __attribute__((always_inline)) { return c1 + kCols * p < x.w ? v + kCols * ES * p : kNowhere; };
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+#pragma unroll
+            for (int p = 0; p < kPieces; p += 2) {
+                v4u lo, hi;
+                if constexpr (F32) {
+                    lo = __builtin_bit_cast(v4u, acc[i][p]);
+                    hi = __builtin_bit_cast(v4u, acc[i][p + 1]);
+                } else {
+                    lo = pack_pair(acc[i][2 * p], acc[i][2 * p + 1]);
+                    hi = pack_pair(acc[i][2 * p + 2], acc[i][2 * p + 3]);
+                }
+                if constexpr (kLines) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t got = __builtin_amdgcn_update_dpp(0u, up ? lo[q] : hi[q], 0x128, 0xf, 0xf, false);   // row_ror:8
+                        lo[q] = up ? got : lo[q];
+                        hi[q] = up ? hi[q] : got;
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(lo, from_row(x, 16 * i), at(p), 0, kNonTemporal);
+                    __builtin_amdgcn_raw_buffer_store_b128(hi, from_row(x, 16 * i + 8), at(p), 0, kNonTemporal);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b128(lo, from_row(x, 16 * i), at(p), 0, kNonTemporal);
+                    __builtin_amdgcn_raw_buffer_store_b128(hi, from_row(x, 16 * i), at(p + 1), 0, kNonTemporal);
+                }
+            }
+            sched_fence();
+        }
     };
     // The sums' start: zero, or what is there (ACC).  Adding it at the end
     // instead would save the sums' roundings at its magnitude (2^-24 of it a
     // step) but needs registers that the fragments hold.
     auto begin = [&](const Part& t) __attribute__((always_inline)) {
         if constexpr (ACC) {
-            if (t.mine)
-                outputs(t, [&](int i, int p, __amdgpu_buffer_rsrc_t r, uint32_t v) __attribute__((always_inline)) {
-                    acc[i][p] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, v, 0, 0));
-                });
+            if (!t.mine) return;
+            const Rows x = rows_of(t);
+            const uint32_t v = (uint32_t)(((lane & 15) * N + c0) * ES);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p)
+                    acc[i][p] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                        from_row(x, 16 * i), c0 + kCols * p < x.w ? v + kCols * ES * p : kNowhere, 0, 0));
         } else {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
