@@ -175,7 +175,8 @@ constexpr int kTab = 2048;    // ints beside it: together the CU's 160 KB
 // One block's tiles t, t + nslots, ... ; all fields are wave-uniform.
 struct Cursor {
     int64_t t;
-    int e, lo, hi;   // the tile's expert and its rows
+    int e;           // the place of the tile's expert in the walk
+    int x, lo, hi;   // the expert and its rows
     int tm, tn;      // the tile's place among the expert's m-tiles and n-tiles
     bool valid;
 };
@@ -218,70 +219,147 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     const int grp = wave >> 2, wn = wave & 3;
     const int N = MODE == kFwd ? n_out : k_in;   // output columns
 
-    // first m-tile of each expert and, where they fit, its rows
-    int* s_tpre = s_tab;
+    // The experts in the order their tiles are walked, and, where they fit,
+    // their rows.  Forward and dgrad: as they come, with the first m-tile of
+    // each.  wgrad: every expert has the same tiles, whose time goes with the
+    // expert's rows, so longest first, in classes of 256 rows (within a class
+    // as they come: the writes of short experts, most of their time, lose 6%
+    // in random order).
     const bool rows_in_lds = 3 * El <= kTab;
+    int* s_at = s_tab;   // first m-tile of an expert (wgrad: the expert at a place)
     int* s_lo = s_tab + El;
     int* s_hi = s_lo + El;
     const int ntm_w = (n_out + BM - 1) / BM;   // wgrad: m-tiles of every expert
-    int nt[2];
+    int lo[2], hi[2], nt[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int e = tid * 2 + j;
-        nt[j] = 0;
         if (e < El) {
-            int lo, hi;
-            segment(offsets, counts, cap_rows, e, lo, hi);
-            if (rows_in_lds) {
-                s_lo[e] = lo;
-                s_hi[e] = hi;
-            }
-            // an expert without rows has a gradient of zeros to write, or nothing to add
-            nt[j] = MODE == kWgrad ? (ACC && hi == lo ? 0 : ntm_w) : (hi - lo + BM - 1) / BM;
+            segment(offsets, counts, cap_rows, e, lo[j], hi[j]);
+            nt[j] = (hi[j] - lo[j] + BM - 1) / BM;
         }
     }
-    const int mtiles = expert_prefix(nt, El, MODE == kWgrad ? (int64_t)El * ntm_w : cap_rows / BM + El, s_tpre,
-                                     reinterpret_cast<int64_t*>(smem));
+    int mtiles;
+    bool alike = true;
+    if constexpr (MODE == kWgrad) {
+        // an expert without rows has a gradient of zeros to write, or (class
+        // 0) nothing to add
+        auto class_of = [](int rows) __attribute__((always_inline)) { return rows > 0 ? (rows + 255) / 256 : ACC ? 0 : 1; };
+        int lo0, hi0, mine[2];
+        segment(offsets, counts, cap_rows, 0, lo0, hi0);
+        const int class0 = class_of(hi0 - lo0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mine[j] = tid * 2 + j < El ? class_of(hi[j] - lo[j]) : class0;
+        int* s_same = reinterpret_cast<int*>(smem);   // of each wave: its experts are of class0
+        const bool same = __all(mine[0] == class0 && mine[1] == class0);
+        if (lane == 0) s_same[wave] = same && class0 > 0;
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) alike = alike && s_same[w] != 0;
+        int walked = El, at[2] = {tid * 2, tid * 2 + 1};
+        if (!alike) {   // places by class
+            int4* s_class = reinterpret_cast<int4*>(smem + 1024);   // El, then -1 up to a multiple of 4
+            const int quads = (El + 3) / 4;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (tid * 2 + j < quads * 4) reinterpret_cast<int*>(s_class)[tid * 2 + j] = tid * 2 + j < El ? mine[j] : -1;
+            __syncthreads();
+            walked = at[0] = at[1] = 0;
+#pragma unroll 4
+            for (int q = 0; q < quads; ++q) {
+                const int4 c = s_class[q];
+                const int other[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    walked += other[i] > 0;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        at[j] += other[i] > mine[j] || (other[i] == mine[j] && q * 4 + i < tid * 2 + j);
+                }
+            }
+            walked = __builtin_amdgcn_readfirstlane(walked);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (tid * 2 + j >= El) continue;
+            s_at[at[j]] = tid * 2 + j;
+            if (rows_in_lds) {
+                s_lo[at[j]] = lo[j];
+                s_hi[at[j]] = hi[j];
+            }
+        }
+        mtiles = ntm_w * walked;
+        __syncthreads();   // the places are read, and the ring loaded, from here on
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = tid * 2 + j;
+            if (rows_in_lds && e < El) {
+                s_lo[e] = lo[j];
+                s_hi[e] = hi[j];
+            }
+        }
+        mtiles = expert_prefix(nt, El, cap_rows / BM + El, s_at, reinterpret_cast<int64_t*>(smem));
+    }
+
+    // Which tiles are this block's: those of an XCD lie side by side, so that
+    // its blocks share operands in its L2.  Where tiles cost alike: the XCD's
+    // eighth of the sequence.  Where they do not: of every round of gridDim.x
+    // tiles the XCD's eighth, so that each has its share of the long ones
+    // (4096 tokens on hot experts, 2048 x 768: 207-235 -> 168 us; 512 tokens,
+    // all short, fp32: 262 us dealt, 246 in eighths).
     const int ntn = (N + BN - 1) / BN;
     const int xcd = blockIdx.x & 7, nslots = gridDim.x >> 3;
-    const int64_t total = (int64_t)mtiles * ntn, t_hi = total * (xcd + 1) / 8;
+    const int64_t total = (int64_t)mtiles * ntn;
+    const int64_t t_lo = alike ? total * xcd / 8 : xcd * nslots;
+    const int64_t t_hi = alike ? total * (xcd + 1) / 8 : total;
+    const int t_step = alike ? nslots : (int)gridDim.x;
 
-    auto place = [&](Cursor& c) __attribute__((always_inline)) {   // c.t lies in expert c.e
-        const int first = __builtin_amdgcn_readfirstlane(s_tpre[c.e]);
-        const int end = c.e + 1 < El ? __builtin_amdgcn_readfirstlane(s_tpre[c.e + 1]) : mtiles;
+    auto place = [&](Cursor& c) __attribute__((always_inline)) {   // c.t lies in the expert at place c.e
+        const int first = MODE == kWgrad ? c.e * ntm_w : __builtin_amdgcn_readfirstlane(s_at[c.e]);
+        const int end = MODE == kWgrad ? first + ntm_w
+                        : c.e + 1 < El ? __builtin_amdgcn_readfirstlane(s_at[c.e + 1]) : mtiles;
         const uint32_t mt = (uint32_t)(end - first);
         const uint32_t local = (uint32_t)(c.t - (int64_t)first * ntn);
         c.tn = (int)(local / mt);
         c.tm = (int)(local - (uint32_t)c.tn * mt);
+        c.x = MODE == kWgrad ? __builtin_amdgcn_readfirstlane(s_at[c.e]) : c.e;
         int lo, hi;
         if (rows_in_lds) {
             lo = s_lo[c.e];
             hi = s_hi[c.e];
         } else {
-            segment(offsets, counts, cap_rows, c.e, lo, hi);
+            segment(offsets, counts, cap_rows, c.x, lo, hi);
         }
         c.lo = __builtin_amdgcn_readfirstlane(lo);
         c.hi = __builtin_amdgcn_readfirstlane(hi);
     };
     auto start = [&](Cursor& c) __attribute__((always_inline)) {
-        c.t = total * xcd / 8 + (blockIdx.x >> 3);
+        c.t = t_lo + (blockIdx.x >> 3);
         c.valid = c.t < t_hi;
-        c.tm = c.tn = c.e = c.lo = c.hi = 0;
+        c.tm = c.tn = c.e = c.x = c.lo = c.hi = 0;
         if (!c.valid) return;
-        int lo = 0, hi = El - 1;   // the last expert whose first tile is not after t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)s_tpre[mid] * ntn <= c.t) lo = mid; else hi = mid - 1;
+        if constexpr (MODE == kWgrad) {
+            c.e = (int)((uint32_t)c.t / (uint32_t)(ntm_w * ntn));
+        } else {
+            int lo = 0, hi = El - 1;   // the last expert whose first tile is not after t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((int64_t)s_at[mid] * ntn <= c.t) lo = mid; else hi = mid - 1;
+            }
+            c.e = __builtin_amdgcn_readfirstlane(lo);
         }
-        c.e = __builtin_amdgcn_readfirstlane(lo);
         place(c);
     };
     auto next = [&](Cursor& c) __attribute__((always_inline)) {
-        c.t += nslots;
+        c.t += t_step;
         c.valid = c.t < t_hi;
         if (!c.valid) return;
-        while (c.e + 1 < El && (int64_t)s_tpre[c.e + 1] * ntn <= c.t) ++c.e;
-        c.e = __builtin_amdgcn_readfirstlane(c.e);
+        if constexpr (MODE == kWgrad) {
+            c.e = (int)((uint32_t)c.t / (uint32_t)(ntm_w * ntn));   // at most 1024 * 256 * 256 tiles
+        } else {
+            while (c.e + 1 < El && (int64_t)s_at[c.e + 1] * ntn <= c.t) ++c.e;
+            c.e = __builtin_amdgcn_readfirstlane(c.e);
+        }
         place(c);
     };
     // a tile's first output row (a row of the buffer; wgrad: of the expert's
@@ -320,8 +398,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         const uint8_t* A = reinterpret_cast<const uint8_t*>(a);
         const uint8_t* B = reinterpret_cast<const uint8_t*>(b);
         dA = MODE == kWgrad ? A + (int64_t)d.lo * ldA + m0 * 2 : A + (int64_t)m0 * ldA;
-        dB = MODE == kFwd ? B + ((int64_t)d.e * n_out + n0) * ldB
-           : MODE == kDgrad ? B + (int64_t)d.e * n_out * ldB + n0 * 2
+        dB = MODE == kFwd ? B + ((int64_t)d.x * n_out + n0) * ldB
+           : MODE == kDgrad ? B + (int64_t)d.x * n_out * ldB + n0 * 2
                             : B + (int64_t)d.lo * ldB + n0 * 2;
     };
     d_tile();
@@ -429,7 +507,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         t.m0 = m_first(c) + grp * 64 * NA;
         t.m_end = MODE == kWgrad ? n_out : c.hi;
         t.n0 = c.tn * BN + wn * 64;
-        t.e = c.e;
+        t.e = c.x;
         t.mine = t.m0 < t.m_end && t.n0 < N;
         return t;
     };
