@@ -434,7 +434,7 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
  * the list overlaps; moe_grad_sumsq does not read the field), numel values (0
  * allowed), dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32 for both.  The list is host
  * memory and is not needed after the call returns; it goes to the kernels by
- * value, 64 tensors a launch. */
+ * value, 128 tensors a launch. */
 typedef struct {
     const void* grad;
     void* out;

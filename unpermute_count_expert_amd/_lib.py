@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes as C
+import operator
 import os
 from typing import Optional
 
@@ -635,28 +636,46 @@ def moe_unpermute_weight_reduce_bwd(dout, y, inv_perm, topk_weights, dy, dweight
            "moe_unpermute_weight_reduce_bwd")
 
 
+_dtype_of = operator.attrgetter("dtype")
 _GRAD_DTYPE = {torch.bfloat16: MOE_DTYPE_BF16, torch.int16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _check_grads(ts, what):
+    """Kinds (MOE_DTYPE_*) of a list of tensors, after the checks: one pass over the list for each, as a model has
+    many small ones and the loop is most of such a call's time."""
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} {i} must be a torch.Tensor, not {type(t).__name__}")
+    kinds = list(map(_GRAD_DTYPE.get, map(_dtype_of, ts)))
+    if None in kinds:
+        i = kinds.index(None)
+        raise TypeError(f"{what} {i} has dtype {ts[i].dtype}; expected bf16 or float32")
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        i = list(map(torch.Tensor.is_contiguous, ts)).index(False)
+        raise ValueError(f"{what} {i} must be contiguous")
+    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for i, d in enumerate(map(torch.Tensor.get_device, ts)):   # -1 on the CPU
+        if d != current:
+            raise ValueError(f"{what} {i} is on {ts[i].device}; the library needs tensors on the current CUDA device")
+    return kinds
 
 
 def _grad_list(grads, outs):
     """The moe_grad_tensor array (four 64-bit words a tensor: grad, out, numel, dtype) of a list of tensors."""
-    words = []
-    current = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        for t in (g,) if o is g else (g, o):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"tensor {i} must be a torch.Tensor, not {type(t).__name__}")
-            if t.dtype not in _GRAD_DTYPE:
-                raise TypeError(f"tensor {i} has dtype {t.dtype}; expected bf16 or float32")
-            if not t.is_contiguous():
-                raise ValueError(f"tensor {i} must be contiguous")
-            if not t.is_cuda or t.get_device() != current:
-                raise ValueError(f"tensor {i} is on {t.device}; the library needs tensors on the current CUDA device")
-        kind = _GRAD_DTYPE[g.dtype]
-        if o is not g and (o.shape != g.shape or _GRAD_DTYPE[o.dtype] != kind):
-            raise ValueError(f"tensor {i}: out has shape {tuple(o.shape)} and dtype {o.dtype}; "
-                             f"expected {tuple(g.shape)} and {g.dtype}")
-        words += (g.data_ptr(), o.data_ptr(), g.numel(), kind)
+    kinds = _check_grads(grads, "gradient")
+    sizes = list(map(torch.Tensor.numel, grads))
+    words = [0] * (4 * len(grads))
+    words[0::4] = map(torch.Tensor.data_ptr, grads)
+    words[2::4] = sizes
+    words[3::4] = kinds
+    if outs is grads:
+        words[1::4] = words[0::4]
+    else:
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
+        if _check_grads(outs, "out") != kinds or list(map(torch.Tensor.numel, outs)) != sizes:
+            raise ValueError("an out has another dtype or number of elements than its gradient")
+        words[1::4] = map(torch.Tensor.data_ptr, outs)
     return array.array("Q", words)
 
 
@@ -682,8 +701,6 @@ def moe_grad_clip(grads, outs, sumsq, max_norm, norm=None, stream=None):
     receives the norm before clipping."""
     grads = list(grads)
     outs = grads if outs is None else list(outs)
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(outs)} outs for {len(grads)} grads")
     check_arg(sumsq, "sumsq", (torch.float64,), (1,))
     check_arg(norm, "norm", F32, (1,), optional=True)
     table = _grad_list(grads, outs)

@@ -620,14 +620,19 @@ int permute_self_count(int64_t nblk) { return nblk <= 16 ? 1 : 0; }
 // 2048 blocks) and at most one slice per group.  Measured on 2048-wide
 // tokens with topk 8: the best slice counts were 16 at 32 and 64 pair
 // blocks, 8 at 128, 4 at 256 and 512 (16384 tokens: 0.095 ms with 1 slice,
-// 0.089 with 4, 0.094 with 8).
-dim3 scatter_grid(int64_t nblk, int K) {
+// 0.089 with 4, 0.094 with 8).  bf16 rows (whole: twice the bytes) take about
+// 512 blocks in all instead: at 4096 bytes and topk 8, slices and us: 64 pair
+// blocks 4 to 16 level (19.5), 16 and 32 slices 19.8 and 27.7; 128 pair blocks
+// 30.2 with 4, 36.6 with 16, 43 with 1; 512 pair blocks (16384 tokens) 134
+// with 1, 161 with 2, 181 with 4; 1024 pair blocks 258 with 1, 263 with 2.
+dim3 scatter_grid(int64_t nblk, int K, bool bf16_rows) {
     const int64_t bx = nblk > 0 ? nblk : 1;
     const int64_t kg = K / kGroup;
     int64_t lo = 2048 / bx;
     lo = lo < 1 ? 1 : (lo > 4 ? 4 : lo);
     int64_t by = 1024 / bx;
     by = by < lo ? lo : by;
+    if (bf16_rows) by = bx < 512 ? 512 / bx : 1;
     by = by > kg ? kg : by;
     const int64_t gps = (kg + by - 1) / by;   // groups per slice; no slice left empty
     return dim3((unsigned)bx, (unsigned)((kg + gps - 1) / gps), 1);
@@ -693,7 +698,7 @@ hipError_t launch_permute(const uint8_t* a_q, const float* a_s, const int32_t* i
         k_permute_colscan<<<(unsigned)El, kScanThreads, 0, s>>>(hist, (int)nblk, El, counts, counts_copy);
     }
     auto* kern = scatter_kernel<false>(emap != nullptr && Eg > kMapLds, self);
-    kern<<<scatter_grid(nblk, K), kPermThreads, 0, s>>>(
+    kern<<<scatter_grid(nblk, K, a_s == nullptr), kPermThreads, 0, s>>>(
         a_q, a_s, nullptr, ids, topk_w, apply_on_input, Mc, K, topk, tpb, emap, Eg, El, bits_for(El), hist,
         counts, counts_copy, align, cap_rows, offsets, a_perm, a_perm_s, inv_perm, row_src);
     return hipGetLastError();
@@ -722,7 +727,7 @@ hipError_t launch_quant_permute(const uint16_t* x, const int32_t* ids, const flo
         k_permute_colscan<<<(unsigned)El, kScanThreads, 0, s>>>(hist, (int)nblk, El, counts, counts_copy);
     }
     auto* kern = scatter_kernel<true>(emap != nullptr && Eg > kMapLds, self);
-    kern<<<scatter_grid(nblk, K), kPermThreads, 0, s>>>(
+    kern<<<scatter_grid(nblk, K, false), kPermThreads, 0, s>>>(
         nullptr, nullptr, x, ids, topk_w, apply_on_input, Mc, K, topk, tpb, emap, Eg, El, bits_for(El), hist,
         counts, counts_copy, align, cap_rows, offsets, a_perm, a_perm_s, inv_perm, row_src);
     return hipGetLastError();

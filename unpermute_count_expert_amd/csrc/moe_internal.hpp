@@ -177,9 +177,9 @@ hipError_t launch_unpermute_bwd(const uint16_t* dout, const uint16_t* y, int64_t
                                 const float* topk_w, int64_t Mc, int K, int topk, uint16_t* dy, float* dweights,
                                 int num_cus, hipStream_t s);
 
-// Tensors of one launch of the gradient kernels; each fills at most
-// kGradBlocks blocks and partial sums.
-constexpr int kGradTensors = 64;
+// Tensors of one launch of the gradient kernels, whose sum of squares leaves
+// at most kGradBlocks partial sums.
+constexpr int kGradTensors = 128;
 constexpr int kGradBlocks = 2048;
 inline size_t grad_workspace(int num_tensors) {
     return (size_t)((num_tensors + kGradTensors - 1) / kGradTensors) * kGradBlocks * sizeof(double);
