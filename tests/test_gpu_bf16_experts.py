@@ -598,3 +598,118 @@ def test_layer_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b), seed
+
+
+# ---- the products over longer walks, other layouts, and side by side ---------------------
+def check_products_on_gpu(cs, n, k, off, cap, hints, seed):
+    """All three products against 64-bit products on the GPU, every expert."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=g, device=DEV)
+    a, dy, w = rn(cap, k).to(BF), (rn(cap, n) * 0.1).to(BF), (rn(len(cs), n, k) * 0.05).to(BF)
+    O, Cn = i32(off), i32(cs)
+    mask = valid_mask(cs, off, cap).to(DEV)
+    for hint in hints:
+        out, dx = sentinel((cap, n)), sentinel((cap, k))
+        dwf, dwb = torch.empty((len(cs), n, k), device=DEV), torch.empty((len(cs), n, k), dtype=BF, device=DEV)
+        moe.moe_grouped_gemm_bf16(a, w, O, Cn, out, hint)
+        moe.moe_grouped_gemm_bf16_dgrad(dy, w, O, Cn, dx, hint)
+        moe.moe_grouped_gemm_bf16_wgrad(dy, a, O, Cn, dwf, 0, hint)
+        moe.moe_grouped_gemm_bf16_wgrad(dy, a, O, Cn, dwb, 0, hint)
+        assert untouched(out, mask.cpu()) and untouched(dx, mask.cpu())
+        for e, c in enumerate(cs):
+            r = slice(off[e], off[e] + c)
+            ae, de, we = a[r].double(), dy[r].double(), w[e].double()
+            wt, dt = we.T.contiguous(), de.T.contiguous()
+            for got, ref, mag, terms, eps in ((out[r], ae @ wt, ae.abs() @ wt.abs(), k, EPS[BF]),
+                                              (dx[r], de @ we, de.abs() @ we.abs(), n, EPS[BF]),
+                                              (dwf[e], dt @ ae, dt.abs() @ ae.abs(), c, EPS[F32]),
+                                              (dwb[e], dt @ ae, dt.abs() @ ae.abs(), c, EPS[BF])):
+                tol = (eps * ref.abs() + terms * 2.0 ** -23 * mag + TINY) * (1 + 2.0 ** -7)
+                assert ((got.double() - ref).abs() <= tol).all(), (hint, e)
+
+
+@pytest.mark.parametrize("cs,n,k", [
+    ([5000, 0, 1, 777, 2048], 1544, 776),             # many tiles a block, experts of unlike length, odd edges
+    ([257, 256, 255, 0, 1, 128, 129, 64, 65], 264, 520),
+    ([40] * 60, 512, 192),                            # experts not a multiple of eight, all of one class
+    ([0, 0, 900], 8, 4096)])
+def test_products_long_walks(cs, n, k):
+    announce("long walks", cs[:9], n, k)
+    off, cap = segments(cs, 32)
+    check_products_on_gpu(cs, n, k, off, cap, (1, 50 * len(cs), 1 << 20), n + k)
+
+
+@pytest.mark.parametrize("n,k", [(65536, 8), (8, 65536), (72, 30000)])
+def test_products_widest(n, k):
+    announce("widest", n, k)
+    cs = [3, 0, 20]
+    off, cap = segments(cs, 16)
+    check_products_on_gpu(cs, n, k, off, cap, (1, 1 << 20), 5)
+
+
+def test_products_on_slots():
+    """Slots of a fixed size, most of each unused (a batched, masked layout)."""
+    cs = [0, 7, 300, 1, 64]
+    check_products_on_gpu(cs, 136, 200, [i * 320 for i in range(6)], 1600, (1, 1 << 20), 6)
+
+
+def test_products_side_by_side():
+    """The same kernels on two streams at once, each with its own tensors."""
+    g = gen(11)
+    cs = [300, 20, 0, 150]
+    off, cap = segments(cs, 16)
+    sets = [(bf((cap, 320), g).to(DEV), bf((cap, 264), g).to(DEV), bf((4, 264, 320), g).to(DEV)) for _ in range(2)]
+    O, Cn = i32(off), i32(cs)
+
+    def run(s, hint):
+        a, dy, w = s
+        out, dx, dw = sentinel((cap, 264)), sentinel((cap, 320)), torch.empty((4, 264, 320), device=DEV)
+        moe.moe_grouped_gemm_bf16(a, w, O, Cn, out, hint)
+        moe.moe_grouped_gemm_bf16_dgrad(dy, w, O, Cn, dx, hint)
+        moe.moe_grouped_gemm_bf16_wgrad(dy, a, O, Cn, dw, 0, hint)
+        return out.view(torch.int16), dx.view(torch.int16), dw
+
+    want = [[run(s, h) for h in (1, 1 << 20)] for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append([run(s, h) for h in (1, 1 << 20)])
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            for p, q in zip(x, y):
+                assert all(torch.equal(a, b) for a, b in zip(p, q))
+
+
+def test_clip_many_tensors_in_a_graph():
+    """Past one launch's list, captured once; the list is not needed after the call."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    grads = [torch.randn(1 + 37 * i % 5000, generator=g, device=DEV) for i in range(300)]
+    outs = [torch.empty_like(t) for t in grads]
+    s, nrm = torch.zeros(1, dtype=F64, device=DEV), torch.zeros(1, device=DEV)
+    ws = torch.empty(moe.moe_grad_workspace_size(300), dtype=torch.uint8, device=DEV)
+
+    def step():
+        moe.moe_grad_sumsq(list(grads), s, ws)
+        moe.moe_grad_clip(list(grads), list(outs), s, 1.0, nrm)
+
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        step()
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for scale in (1.0, 0.25, 3.0):
+        for t in grads:
+            t.mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = sum(float((t.double() ** 2).sum()) for t in grads)
+        assert abs(float(s) - ref) <= 1e-12 * ref
+        c = min(1.0, 1.0 / (ref ** 0.5 + 1e-6))
+        for t, o in zip(grads, outs):
+            want = t.double() * c
+            assert ((o.double() - want).abs() <= 5 * 2.0 ** -24 * want.abs()).all()

@@ -43,7 +43,9 @@
 //    reads), a prefetch of later steps into L2 (slower by its own reads: the
 //    loads are bound by their number), raised wave priority around the
 //    multiplies (level), loads issued by the multiplying group as well (0.82
-//    ms: its issue slots are what the MFMAs need).
+//    ms: its issue slots are what the MFMAs need), leaving out the multiplies
+//    of a tile's row blocks past the last valid row (level: such tiles wait
+//    for their weights).
 //  * The weight-side fragment is the MFMA's first operand, so a lane holds
 //    four consecutive columns of one row; for bf16 two column blocks are
 //    exchanged between neighbouring 16-lane rows (v_permlane16_swap) to 16
