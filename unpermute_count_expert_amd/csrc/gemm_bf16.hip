@@ -37,7 +37,10 @@
 //    multiplies alone 0.64 ms.  The ring takes the loads alone to 0.45 ms,
 //    the groups the multiplies alone to 0.55 ms and both together to 0.75 ms
 //    (1100 TFLOP/s).  Past that the clock gives: at 64% of the MFMA rate it
-//    is down to 1.5-1.8 GHz (dgrad and wgrad, at 50%, run at 2.0 GHz).
+//    is down to 1.5-1.8 GHz, and a step's fragment reads and loads take the
+//    LDS as many cycles (98 KB out and 32 KB in a phase, 128 bytes a cycle)
+//    as the phase's MFMAs take the matrix units.  dgrad runs at 1070, wgrad
+//    at 920 (fp32 gradients) and 1060 TFLOP/s (bf16).
 //  * Not kept: four waves of 128 x 128 with fragments double-buffered (one
 //    wave per SIMD; 0.96 ms), steps of 32 in four stages (0.96 ms, half-line
 //    reads), a prefetch of later steps into L2 (slower by its own reads: the
@@ -154,10 +157,13 @@ __device__ __forceinline__ int swz(int c, int r) { return c ^ (r & 7) ^ ((r >> 3
 __device__ __forceinline__ int fx(int k) { return ((k >> 1) & 1) | (((k >> 4) & 1) << 1); }
 
 // 16 output indexes by 32 contraction indexes at LDS byte `at` (column
-// layout): contraction rows k..k+3 and k+4..k+7 of the lane's row group
-__device__ __forceinline__ v8bf read_columns(uint32_t at) {
-    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(uintptr_t)at);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(uintptr_t)(at + 512));
+// layout): contraction rows k..k+3 and k+4..k+7 of the lane's row group.
+// __restrict__ tells the compiler that what is read here is not what a load
+// in flight writes (each granule has its own wait); without it, it waits for
+// every load to LDS before the first transposing read of a step.
+__device__ __forceinline__ v8bf read_columns(lds_v4 __restrict__ p) {
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + 512 / sizeof(v4s));
     return __builtin_bit_cast(v8bf, v8s{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
 }
 
@@ -449,6 +455,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         for (int p = R; p < R + NA; ++p) put(p);
         advance();
     };
+    // A reading phase's loads: issued before its transposing reads, which are
+    // many (a wave's 48 in wgrad, 32 with the rows' in dgrad), or after its
+    // plain reads (24).  16384 tokens, 1536 x 2048: dgrad 765 us before, 782
+    // after; wgrad fp32 881 and 978, bf16 765 and 852; forward 768 and 746.
+    auto puts = [&]() __attribute__((always_inline)) {
+        if (grp == 0) even_puts();
+        else odd_puts();
+    };
     // the ring but for what the first even phase loads
     if (grp == 0) {
 #pragma unroll
@@ -472,7 +486,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     };
     // block blk (16 output indexes) and half ks of a granule's contraction
     auto frag = [&](bool T, uint32_t at, int blk, int ks) __attribute__((always_inline)) {
-        return T ? read_columns((at ^ (uint32_t)(blk << 5)) + ks * 1024)
+        return T ? read_columns((lds_v4)(uintptr_t)((at ^ (uint32_t)(blk << 5)) + ks * 1024))
                  : *(lds_v8)(uintptr_t)((at ^ (uint32_t)(ks << 4)) + blk * 2048);
     };
     v4f acc[MI][NJ];
@@ -624,6 +638,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         bool first = true;
         do {   // an expert without rows: one step, of zeros
             to_read();
+            if (BT) puts();
+            sched_fence();
             if (first) {
                 if (have) store();
                 sched_fence();
@@ -634,8 +650,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
             }
             v8bf fa[2][MI], fb[2][NJ];   // the step's fragments: dead between steps, where the stores need registers
             if (t.mine) load(fa, fb);
-            if (grp == 0) even_puts();
-            else odd_puts();
+            if (!BT) puts();
             c_q = c_q + P >= kRing ? c_q + P - kRing : c_q + P;
             to_multiply();
             if (t.mine) multiply(fa, fb);
@@ -782,7 +797,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
                 fa[ks] = *(lds_v8)(uintptr_t)(at + kW + (rA ^ (uint32_t)(ks << 4)));
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
-                    fb[ks][j] = BT ? read_columns(at + (rB ^ (uint32_t)(j << 5)))
+                    fb[ks][j] = BT ? read_columns((lds_v4)(uintptr_t)(at + (rB ^ (uint32_t)(j << 5))))
                                    : *(lds_v8)(uintptr_t)(at + (rB ^ (uint32_t)(ks << 4)) + j * 2048);
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is in registers: refill it
