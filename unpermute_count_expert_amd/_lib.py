@@ -638,14 +638,16 @@ def moe_unpermute_weight_reduce_bwd(dout, y, inv_perm, topk_weights, dy, dweight
 
 _dtype_of = operator.attrgetter("dtype")
 _GRAD_DTYPE = {torch.bfloat16: MOE_DTYPE_BF16, torch.int16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+_PLAIN_TENSORS = {torch.Tensor, torch.nn.Parameter}   # without a look at their bases
 
 
 def _check_grads(ts, what):
     """Kinds (MOE_DTYPE_*) of a list of tensors, after the checks: one pass over the list for each, as a model has
     many small ones and the loop is most of such a call's time."""
-    for i, t in enumerate(ts):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{what} {i} must be a torch.Tensor, not {type(t).__name__}")
+    if not set(map(type, ts)) <= _PLAIN_TENSORS:
+        for i, t in enumerate(ts):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{what} {i} must be a torch.Tensor, not {type(t).__name__}")
     kinds = list(map(_GRAD_DTYPE.get, map(_dtype_of, ts)))
     if None in kinds:
         i = kinds.index(None)
@@ -654,9 +656,10 @@ def _check_grads(ts, what):
         i = list(map(torch.Tensor.is_contiguous, ts)).index(False)
         raise ValueError(f"{what} {i} must be contiguous")
     current = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for i, d in enumerate(map(torch.Tensor.get_device, ts)):   # -1 on the CPU
-        if d != current:
-            raise ValueError(f"{what} {i} is on {ts[i].device}; the library needs tensors on the current CUDA device")
+    devices = list(map(torch.Tensor.get_device, ts))   # -1 on the CPU
+    if devices.count(current) != len(ts):
+        i = next(i for i, d in enumerate(devices) if d != current)
+        raise ValueError(f"{what} {i} is on {ts[i].device}; the library needs tensors on the current CUDA device")
     return kinds
 
 
