@@ -391,8 +391,9 @@ int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int
  *   dw[e,n,k] = sum over e's valid rows r of dy[r,n] * a[r,k]
  * (0 for an expert without rows), in fp32 or rounded once to bf16
  * (dw_dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16).  accumulate = 1 (fp32 only)
- * adds it to what dw holds, which is where the fp32 sum then starts.  dy [cap_rows,n_out], a [cap_rows,k_in] bf16,
- * dw [El,n_out,k_in]; dw overlaps neither input. */
+ * adds it to what dw holds, which is where the fp32 sum then starts.
+ * dy [cap_rows,n_out], a [cap_rows,k_in] bf16, dw [El,n_out,k_in]; dw
+ * overlaps neither input. */
 #define MOE_DTYPE_BF16 0
 #define MOE_DTYPE_F32 1
 int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* expert_offsets,
@@ -421,9 +422,10 @@ int moe_silu_mul_bwd(const uint16_t* h, const uint16_t* dact, int64_t rows, int3
  *   dy[row,c] = bf16( topk_weights[t,k] * dout[t,c] ),
  *   dweights[t,k] = sum_c y[row,c] * dout[t,c]  (fp32),
  * and dweights[t,k] = 0 for the other pairs.  dout [Mc,K], y and dy
- * [y_rows,K] bf16 (rows that no pair names are not written; a row named by
- * two pairs receives either), inv_perm, topk_weights and dweights [Mc,topk].
- * K: positive multiple of 128.  dy overlaps neither dout nor y. */
+ * [y_rows,K] bf16 (rows that no pair names are not written; in a row named by
+ * two pairs each element is either's), inv_perm, topk_weights and dweights
+ * [Mc,topk].  K: positive multiple of 128 up to 65536.  Neither dy nor
+ * dweights overlaps any other argument. */
 int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows,
                                     const int32_t* inv_perm, const float* topk_weights, int64_t Mc, int32_t K,
                                     int32_t topk, uint16_t* dy, float* dweights, void* stream);
@@ -431,7 +433,8 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
 /* Global gradient norm over many tensors, and clipping.  A tensor of the
  * list: `grad` its values (contiguous, aligned to its element only), `out`
  * where moe_grad_clip writes (grad itself, or memory that no other field of
- * the list overlaps; moe_grad_sumsq does not read the field), numel values (0
+ * the list, the sum or the norm overlaps; moe_grad_sumsq does not read the
+ * field), numel values (0
  * allowed), dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32 for both.  The list is host
  * memory and is not needed after the call returns; it goes to the kernels by
  * value, 128 tensors a launch. */

@@ -86,7 +86,9 @@ def unp(dout=P[0], y=P[1], rows=16, inv=P[2], tw=P[3], M=4, K=128, topk=2, dy=P[
     (dict(M=-1), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=1 << 31), SHAPE), (dict(K=64), SHAPE), (dict(K=0), SHAPE),
     (dict(topk=0), SHAPE), (dict(topk=257), SHAPE), (dict(M=1 << 31), SHAPE), (dict(dout=None), ARG),
     (dict(y=None), ARG), (dict(inv=None), ARG), (dict(tw=None), ARG), (dict(dy=None), ARG), (dict(dw=None), ARG),
-    (dict(dy=P[1]), ARG), (dict(dy=P[0]), ARG), (dict(dy=ODD), ARG)])
+    (dict(dy=P[1]), ARG), (dict(dy=P[0]), ARG), (dict(dy=ODD), ARG), (dict(K=65664), SHAPE), (dict(dw=P[3]), ARG),
+    (dict(dw=P[2]), ARG), (dict(dw=P[0]), ARG), (dict(dw=P[1]), ARG), (dict(dw=P[4]), ARG), (dict(dy=P[3]), ARG),
+    (dict(dy=P[2]), ARG)])
 def test_unpermute_bwd_refuses(kw, status):
     assert unp(**kw) == status
 
@@ -145,6 +147,9 @@ def test_clip_refuses_overlapping_memory():
     assert clip((G, 2 * G, 100, 1, 0), (3 * G, 2 * G + 396, 9, 1, 0)) == ARG   # two outs
     assert clip((G, 2 * G, 100, 1, 0), (2 * G + 396, 3 * G, 9, 1, 0)) == ARG   # an out over another's grad
     assert clip((2 * G + 40, 3 * G, 9, 1, 0), (G, 2 * G, 100, 1, 0)) == ARG    # inside, listed first
+    assert clip((G, 2 * G, 100, 1, 0), norm=P[6]) == ARG                       # the norm over the sum
+    assert clip((G, 2 * G, 100, 1, 0), sumsq=C.c_void_p(2 * G + 16)) == ARG    # an out over the sum
+    assert clip((G, G, 100, 1, 0), norm=C.c_void_p(G + 16)) == ARG             # the norm in a tensor
 
 
 def test_workspace_size():

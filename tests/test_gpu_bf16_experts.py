@@ -359,6 +359,29 @@ def test_unpermute_bwd(M, topk, K, rows):
     close(dy.cpu()[r], ref, ref.abs(), 1, "dy bf16")
 
 
+def test_unpermute_bwd_many_tokens():
+    """More tokens (4.3 M) than one launch has waves for: each wave takes several."""
+    M, K = (1 << 22) + 100_001, 128
+    announce("unpermute_bwd", M, 1, K, "many tokens")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device=DEV, dtype=torch.int8)   # exact in small integers
+    y, dout, tw = ints(M, K).to(BF), ints(M, K).to(BF), ints(M, 1).float()
+    inv = torch.randperm(M, generator=g, device=DEV).to(I32)[:, None]
+    inv[7] = -1
+    row7 = torch.ones(M, dtype=torch.bool, device=DEV).index_fill_(0, inv[inv >= 0].long(), False).nonzero()[0, 0]
+    dy, dtw = torch.full((M, K), 9.0, dtype=BF, device=DEV), torch.full((M, 1), 9.0, device=DEV)
+    moe.moe_unpermute_weight_reduce_bwd(dout, y, inv, tw, dy, dtw)
+    torch.cuda.synchronize()
+    assert (dy[row7] == 9).all() and dtw[7, 0] == 0
+    dy[row7] = 0
+    tw[7], inv[7, 0] = 0, row7
+    want = dout * tw.to(BF)
+    assert torch.equal(dy[inv[:, 0].long()], want)
+    dtw[7, 0] = (y[row7].float() * dout[7].float()).sum()
+    assert torch.equal(dtw[:, 0], (y[inv[:, 0].long()].float() * dout.float()).sum(1))
+
+
 def test_unpermute_bwd_matches_differences():
     """out is linear in y and in the weights: exact in small integers."""
     g = gen(4)

@@ -1021,17 +1021,21 @@ int check_grads(const moe_grad_tensor* t, int32_t num, bool clip) {
 }
 
 // Refuses a clip list in which memory that one tensor's `out` covers is any
-// other tensor's grad or out: the result would depend on which block comes
-// first.  The same gradient read twice is fine.
-int check_grad_overlap(const moe_grad_tensor* t, int32_t num) {
+// other tensor's grad or out, the sum or the norm (or the norm is the sum's):
+// the result would depend on which block comes first.  The same gradient read
+// twice is fine.
+int check_grad_overlap(const moe_grad_tensor* t, int32_t num, const double* sumsq, const float* norm) {
     struct Span {
         uintptr_t lo, hi;
         int32_t i;
         bool write;
     };
-    Span* v = num > 0 ? static_cast<Span*>(std::malloc(2 * (size_t)num * sizeof(Span))) : nullptr;
-    REQUIRE(num == 0 || v != nullptr, MOE_ERR_INVALID_ARG, "no host memory for a list of %d tensors", num);
+    Span* v = static_cast<Span*>(std::malloc(2 * ((size_t)num + 1) * sizeof(Span)));
+    REQUIRE(v != nullptr, MOE_ERR_INVALID_ARG, "no host memory for a list of %d tensors", num);
+    const uintptr_t s = reinterpret_cast<uintptr_t>(sumsq), w = reinterpret_cast<uintptr_t>(norm);
     int n = 0;
+    v[n++] = Span{s, s + sizeof(double), num, false};
+    if (w) v[n++] = Span{w, w + sizeof(float), num, true};
     for (int32_t i = 0; i < num; ++i) {
         const uintptr_t bytes = (uintptr_t)t[i].numel * (t[i].dtype == MOE_DTYPE_F32 ? 4 : 2);
         const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), o = reinterpret_cast<uintptr_t>(t[i].out);
@@ -1048,7 +1052,8 @@ int check_grad_overlap(const moe_grad_tensor* t, int32_t num) {
         if (v[j].write) written = v[j].hi > written ? v[j].hi : written;
     }
     std::free(v);
-    REQUIRE(bad < 0, MOE_ERR_INVALID_ARG, "tensor %d: its memory overlaps another tensor's that is written", bad);
+    REQUIRE(bad != num, MOE_ERR_INVALID_ARG, "sumsq or norm overlaps memory that is written");
+    REQUIRE(bad < 0, MOE_ERR_INVALID_ARG, "tensor %d: its memory overlaps other memory that is written", bad);
     return MOE_OK;
 }
 
@@ -1163,7 +1168,8 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
                                     int32_t topk, uint16_t* dy, float* dweights, void* stream) {
     REQUIRE(Mc >= 0 && y_rows >= 0 && y_rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "Mc=%lld y_rows=%lld",
             (long long)Mc, (long long)y_rows);
-    REQUIRE(K > 0 && K % moe::kGroup == 0, MOE_ERR_SHAPE, "K=%d is not a positive multiple of 128", K);
+    REQUIRE(K > 0 && K % moe::kGroup == 0 && K <= 65536, MOE_ERR_SHAPE,
+            "K=%d is not a positive multiple of 128 up to 65536", K);
     REQUIRE(topk >= 1 && topk <= 256, MOE_ERR_SHAPE, "topk=%d outside [1,256]", topk);
     REQUIRE(Mc < (int64_t(1) << 31) / topk, MOE_ERR_SHAPE, "too many tokens");
     if (Mc == 0) return MOE_OK;
@@ -1178,6 +1184,12 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
     const size_t y_b = (size_t)y_rows * K * 2;
     REQUIRE(!overlaps(dy, y_b, y, y_b) && !overlaps(dy, y_b, dout, (size_t)Mc * K * 2), MOE_ERR_INVALID_ARG,
             "dy overlaps an input");
+    const size_t p_b = (size_t)Mc * topk * 4;
+    REQUIRE(!overlaps(dweights, p_b, topk_weights, p_b) && !overlaps(dweights, p_b, inv_perm, p_b) &&
+                !overlaps(dweights, p_b, dout, (size_t)Mc * K * 2) && !overlaps(dweights, p_b, y, y_b) &&
+                !overlaps(dweights, p_b, dy, y_b) && !overlaps(dy, y_b, topk_weights, p_b) &&
+                !overlaps(dy, y_b, inv_perm, p_b),
+            MOE_ERR_INVALID_ARG, "dweights overlaps another argument, or dy the indices or weights");
     int cus = 0;
     int st = check_device(&cus);
     if (st) return st;
@@ -1212,11 +1224,12 @@ int moe_grad_sumsq(const moe_grad_tensor* tensors, int32_t num_tensors, double* 
 int moe_grad_clip(const moe_grad_tensor* tensors, int32_t num_tensors, const double* sumsq, float max_norm,
                   float* norm, void* stream) {
     int st = check_grads(tensors, num_tensors, true);
-    if (!st) st = check_grad_overlap(tensors, num_tensors);
     if (st) return st;
     REQUIRE(max_norm >= 0.0f, MOE_ERR_INVALID_ARG, "max_norm=%g is negative or NaN", (double)max_norm);
     REQUIRE_PTR(sumsq);
     if (norm) REQUIRE_PTR(norm);
+    st = check_grad_overlap(tensors, num_tensors, sumsq, norm);
+    if (st) return st;
     st = check_device(nullptr);
     if (st) return st;
     HIP_OK(moe::launch_grad_clip(tensors, num_tensors, sumsq, max_norm, norm, static_cast<hipStream_t>(stream)));

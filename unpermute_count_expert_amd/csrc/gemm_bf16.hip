@@ -65,6 +65,9 @@
 // streaming its own share through its own three LDS stages without barriers,
 // the four sums added in a fixed order.  One token, top-8, 1536 x 2048 (50 MB
 // of weights): 11.9 us against 31 us on k_tiles; 64 tokens 137 against 169.
+#include <algorithm>
+#include <cmath>
+
 #include "moe_device.hpp"
 #include "moe_internal.hpp"
 
@@ -203,7 +206,7 @@ struct Cursor {
 // the loads that a wave has issued after the one needed; they are exact,
 // because past the last tile the stream goes on with loads of zero bytes.
 // F32: fp32 outputs; ACC: added to what is there.
-template <int MODE, int NA, bool F32, bool ACC>
+template <int MODE, int NA, bool F32, bool ACC, bool TURN>   // TURN: forward only
 __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
                                                        const int32_t* __restrict__ offsets,
                                                        const int32_t* __restrict__ counts, int El, int64_t cap_rows,
@@ -395,6 +398,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     if (!d.valid) return;   // no tile for this block
     const uint8_t *dA, *dB;   // the step's operands
     int d_left, tA, tB;       // contraction left; operand bytes that do not depend on the step
+    // TURN: neighbouring tiles start a step apart and go round the
+    // contraction.  In step they would all read the same 128 bytes of their
+    // rows at a time, which for rows of 4 KB lie on a few of the memory's
+    // channels.  Forward, 1536 x 2048, 128 experts, rows per expert and us in
+    // step and turned: 16 150-182 and 139, 64 162-189 and 155, 187 227 and 191;
+    // where the products bound, the turn only costs the rows' reuse: 256 272 and
+    // 277, 1024 738 and 764.
+    const int nsteps = (k_in + BK - 1) / BK;
+    int d_cnt = 0;            // TURN: the tile's steps left
     int d_q = 0;              // ring slot of the step's granule 0
     const int gA = AT ? 128 : 64 * ldA, gB = BT ? 128 : 64 * ldB;   // bytes between granules in memory
     auto d_tile = [&]() __attribute__((always_inline)) {
@@ -409,6 +421,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         dB = MODE == kFwd ? B + ((int64_t)d.x * n_out + n0) * ldB
            : MODE == kDgrad ? B + (int64_t)d.x * n_out * ldB + n0 * 2
                             : B + (int64_t)d.lo * ldB + n0 * 2;
+        if constexpr (TURN) {
+            d_cnt = nsteps;
+            const int first = (int)((uint32_t)(d.e * ntn + d.tn) % (uint32_t)nsteps);
+            dA += first * BK * 2;
+            dB += first * BK * 2;
+            d_left -= first * BK;
+        }
     };
     d_tile();
     auto put = [&](int p) __attribute__((always_inline)) {   // granule p of the step
@@ -433,12 +452,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         dB += BT ? (int64_t)BK * ldB : BK * 2;
         d_left -= BK;
         d_q = d_q + P >= kRing ? d_q + P - kRing : d_q + P;
-        if (d_left <= 0) {
+        if (TURN && --d_cnt > 0) {
+            if (d_left <= 0) {
+                dA -= nsteps * BK * 2;
+                dB -= nsteps * BK * 2;
+                d_left = k_in;
+            }
+        } else if (TURN || d_left <= 0) {
             if (d.valid) next(d);
             if (d.valid) {
                 d_tile();
             } else {   // past the last tile: zero bytes
                 d_left = 0;
+                d_cnt = 1;
                 tA = tB = -(1 << 30);
             }
         }
@@ -546,12 +572,26 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     auto from_row = [&](const Rows& x, int r) __attribute__((always_inline)) {
         return __builtin_amdgcn_make_buffer_rsrc(x.o + (int64_t)r * N * ES, 0, max(x.bytes - r * N * ES, 0), 0x00020000);
     };
-    // Non-temporal stores: what is written is read again from HBM, and a
-    // gradient's bytes are most of a short batch's time.  There (kLines) the
+    // A gradient's bytes are most of a short batch's time.  There (kLines) the
     // lanes eight apart trade halves of two neighbouring pieces, so that a
     // store writes eight rows of whole 128-byte lines instead of sixteen of
     // half lines (512 tokens, 1536 x 2048: fp32 gradients 290 -> 245 us, bf16
-    // 234 -> 149; forward and dgrad are level or 3% slower with it).
+    // 234 -> 149; forward and dgrad are level or 3% slower with it), and
+    // non-temporal where the rows are whole lines (4096 tokens on hot experts,
+    // 2048 x 768, bf16: 150 us, plainly 202).  Where they are not, a piece's
+    // two half-filled lines have to meet their other halves in L2: plain
+    // stores (725 tokens, 704 x 1256: fp32 208 -> 107 us, bf16 104 -> 43).
+    // The rows' products are written once and read soon: plainly in the
+    // forward (16384 tokens, 736 against 746 us non-temporal; 60 experts of
+    // 408 x 336, 31 against 37), non-temporal in dgrad (4096 tokens on hot
+    // experts 150 against 155 us, widths of half lines 3% slower).
+    const bool whole = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(N * ES)) & 127) == 0;
+    auto put16 = [&](const v4u& v, const __amdgpu_buffer_rsrc_t& r, uint32_t at) __attribute__((always_inline)) {
+        if (MODE == kDgrad || (MODE == kWgrad && whole))
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, kNonTemporal);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
+    };
     auto store = [&]() __attribute__((always_inline)) {
         if (!done.mine) return;
         constexpr bool kLines = MODE == kWgrad;
@@ -579,11 +619,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
                         lo[q] = up ? got : lo[q];
                         hi[q] = up ? hi[q] : got;
                     }
-                    __builtin_amdgcn_raw_buffer_store_b128(lo, from_row(x, 16 * i), at(p), 0, kNonTemporal);
-                    __builtin_amdgcn_raw_buffer_store_b128(hi, from_row(x, 16 * i + 8), at(p), 0, kNonTemporal);
+                    put16(lo, from_row(x, 16 * i), at(p));
+                    put16(hi, from_row(x, 16 * i + 8), at(p));
                 } else {
-                    __builtin_amdgcn_raw_buffer_store_b128(lo, from_row(x, 16 * i), at(p), 0, kNonTemporal);
-                    __builtin_amdgcn_raw_buffer_store_b128(hi, from_row(x, 16 * i), at(p + 1), 0, kNonTemporal);
+                    put16(lo, from_row(x, 16 * i), at(p));
+                    put16(hi, from_row(x, 16 * i), at(p + 1));
                 }
             }
             sched_fence();
@@ -837,19 +877,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
     wait_loads<0>();   // no load may still write this block's LDS when it ends
 }
 
-// Which kernel, by the rows expected per expert, r = rows_hint / El.  Measured
-// on 128 experts, top-8, 1536 x 2048 (forward / dgrad, us; k_few, k_tiles of
-// 128 rows, of 256 rows):
-//   r 4   137 / 147   169 / 138   177 / 143
-//   r 8   139 / 152   180 / 139   190 / 142      (768 x 2048, r 8: 78 / 75   76 / 90   80 / 95)
-//   r 16  156 / 183   156 / 142   159 / 143
-//   r 32  217 / 252   184 / 139   193 / 144
-//   r 96  470 / 520   198 / 155   200 / 165
-//   r 128 605 / 718   220 / 225   215 / 184
-// and on 8 experts of 4096 x 4096: r 2 47 / 43, 66 / 68; r 8 52 / 54, 72 / 74;
-// r 32 64 / 75, 59 / 60.  So k_few up to 8 rows, 128-row tiles below 104,
-// 256-row tiles from there on, whatever the direction.  The gradient by the
-// weights has whole matrices as output tiles and takes 256-row tiles always.
+// Which kernel.  Where there are many weights their bytes bound both alike;
+// what tells the kernels apart is how well their units of work fill the CUs
+// and how long one takes.  The rule compares estimates of that in
+// microseconds, for rows_hint rows spread evenly and a part of a tile more an
+// expert for raggedness; the constants are fitted to 538 measured calls (1 to
+// 131072 rows, 4 to 128 experts, widths of 128 to 4096, even and skewed
+// routing), in which the choice is 1.2% slower than the best of the three on
+// average (by rows per expert alone 9%).  Measured (k_few, 128 rows, 256 rows;
+// r rows per expert):
+//   128 experts, 1536 x 2048, forward   r 4  138 139 142   r 16 158 143 144
+//                                       r 96 480 160 162   r 128 616 211 177
+//                             dgrad     r 4  149 142 141   r 16 171 145 140
+//                                       r 96 465 155 168   r 128 608 215 171
+//   8 experts, 4096 x 4096, forward     r 8   52  70  83   r 32  67  61  79   r 250 351 144 94
+//   8 experts, 1504 x 488, forward      r 1    6  12  15
+//   8 experts, 624 x 176, dgrad         r 139  7  14  18
+//   16 experts, 352 x 200, forward      r 275 17  11  13
+//   4 experts, 376 x 1360, forward      r 41   9  24  31
+//   32 experts, 1792 x 1376, forward    r 106 113 57  71
+// The gradient by the weights has whole matrices as output tiles: 128-row
+// ones while those are at most one and a half a CU (16 experts of 352 x 200,
+// 4404 rows: 42 us against 59; 8 of 624 x 176, 1110 rows: 8.7 and 11.8), past
+// that 256-row ones (32 experts of 1792 x 1376, bf16: 53 us against 56; 128 of
+// 1536 x 2048, 32768 rows: 288 and 340).
+// Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
 template <int MODE, bool F32, bool ACC>
 hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
                   int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, void* out, int num_cus, hipStream_t s) {
@@ -857,13 +909,30 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
     auto tiles = [&](auto* kernel) {
         kernel<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, out);
     };
+    const double cus = num_cus;
+    const int ntn = ((MODE == kFwd ? n_out : k_in) + BN - 1) / BN;   // n-tiles
     if constexpr (MODE == kWgrad) {
-        tiles(k_tiles<MODE, 2, F32, ACC>);
+        if ((double)El * ((n_out + 127) / 128) * ntn <= 1.5 * cus) tiles(k_tiles<MODE, 1, F32, ACC, false>);
+        else tiles(k_tiles<MODE, 2, F32, ACC, false>);
     } else {
-        if (rows_hint >= (int64_t)104 * El) tiles(k_tiles<MODE, 2, F32, ACC>);
-        else if (rows_hint > (int64_t)8 * El) tiles(k_tiles<MODE, 1, F32, ACC>);
-        else k_few<MODE><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
-                                                    static_cast<uint16_t*>(out));
+        constexpr int NC = MODE == kDgrad ? 64 : 32, KS = MODE == kDgrad ? 32 : 64;   // k_few's columns and step
+        const int N = MODE == kFwd ? n_out : k_in, C = MODE == kFwd ? k_in : n_out;
+        const double experts = rows_hint < El ? (double)rows_hint : El, r = (double)rows_hint / experts;
+        const double bytes = experts * N * C * 2 / 5.5e6;   // the weights' time
+        const double units = experts * std::max(1.0, r / 16 + 0.75) * ((N + NC - 1) / NC) / (2 * cus);
+        const double few = 3.5 + std::max(1.0, units) *
+                                     (1.5 + (MODE == kDgrad ? 1.2 : 0.85) * ((C + 4 * KS - 1) / (4 * KS)));
+        // rounds of tiles; 128 rows unless 256 save more than a fifth of them
+        const double rounds1 = experts * std::max(1.0, r / 128 + 0.5) * ntn / cus;
+        const double rounds2 = experts * std::max(1.0, r / 256 + 0.5) * ntn / cus;
+        const bool low = 4 * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
+        const double walk = 6.5 + std::max(1.0, low ? rounds1 : rounds2) * (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
+        if (std::max(few, bytes) <= std::max(walk, bytes + 1))
+            k_few<MODE><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
+                                                  static_cast<uint16_t*>(out));
+        else if (low) tiles(k_tiles<MODE, 1, F32, ACC, MODE == kFwd>);
+        else if (MODE == kFwd && rows_hint < (int64_t)208 * El) tiles(k_tiles<MODE, 2, F32, ACC, MODE == kFwd>);
+        else tiles(k_tiles<MODE, 2, F32, ACC, false>);
     }
     return hipGetLastError();
 }
