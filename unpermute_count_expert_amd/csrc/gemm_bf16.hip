@@ -64,7 +64,7 @@
 // in dgrad) columns per four waves that split the contraction, each wave
 // streaming its own share through its own three LDS stages without barriers,
 // the four sums added in a fixed order.  One token, top-8, 1536 x 2048 (50 MB
-// of weights): 11.9 us against 31 us on k_tiles; 64 tokens 137 against 169.
+// of weights): 11.9 us against 31 us on k_tiles.
 #include <algorithm>
 #include <cmath>
 
@@ -896,11 +896,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 //   16 experts, 352 x 200, forward      r 275 17  11  13
 //   4 experts, 376 x 1360, forward      r 41   9  24  31
 //   32 experts, 1792 x 1376, forward    r 106 113 57  71
-// The gradient by the weights has whole matrices as output tiles: 128-row
-// ones while those are at most one and a half a CU (16 experts of 352 x 200,
-// 4404 rows: 42 us against 59; 8 of 624 x 176, 1110 rows: 8.7 and 11.8), past
-// that 256-row ones (32 experts of 1792 x 1376, bf16: 53 us against 56; 128 of
-// 1536 x 2048, 32768 rows: 288 and 340).
+// The gradient by the weights has whole matrices as output tiles; 256-row ones
+// where they save more than two fifths of the rounds (290 calls: 1.2% slower
+// than the better on average, always 256 rows 11%; 16 experts of 352 x 200,
+// 4404 rows: 42 us with 128 rows, 59 with 256; 128 of 264 x 360, 16384 rows: 63
+// and 86; 128 of 1536 x 2048, 32768 rows, bf16: 340 and 288).
 // Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
 template <int MODE, bool F32, bool ACC>
 hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
@@ -912,7 +912,9 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
     const double cus = num_cus;
     const int ntn = ((MODE == kFwd ? n_out : k_in) + BN - 1) / BN;   // n-tiles
     if constexpr (MODE == kWgrad) {
-        if ((double)El * ((n_out + 127) / 128) * ntn <= 1.5 * cus) tiles(k_tiles<MODE, 1, F32, ACC, false>);
+        const double rounds1 = std::ceil((double)El * ((n_out + 127) / 128) * ntn / cus);
+        const double rounds2 = std::ceil((double)El * ((n_out + 255) / 256) * ntn / cus);
+        if (3 * rounds1 <= 5 * rounds2) tiles(k_tiles<MODE, 1, F32, ACC, false>);
         else tiles(k_tiles<MODE, 2, F32, ACC, false>);
     } else {
         constexpr int NC = MODE == kDgrad ? 64 : 32, KS = MODE == kDgrad ? 32 : 64;   // k_few's columns and step
@@ -926,7 +928,8 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
         const double rounds1 = experts * std::max(1.0, r / 128 + 0.5) * ntn / cus;
         const double rounds2 = experts * std::max(1.0, r / 256 + 0.5) * ntn / cus;
         const bool low = 4 * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
-        const double walk = 6.5 + std::max(1.0, low ? rounds1 : rounds2) * (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
+        const double walk = 6.5 + std::max(1.0, low ? rounds1 : rounds2) *
+                                      (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
         if (std::max(few, bytes) <= std::max(walk, bytes + 1))
             k_few<MODE><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
                                                   static_cast<uint16_t*>(out));
