@@ -662,6 +662,31 @@ def test_products_long_walks(cs, n, k):
     check_products_on_gpu(cs, n, k, off, cap, (1, 50 * len(cs), 1 << 20), n + k)
 
 
+@pytest.mark.parametrize("n,k", [(504, 520), (504, 576), (512, 40), (520, 1032)])
+def test_products_every_kernel(n, k):
+    """Enough experts that the row count given picks each kernel in turn (a few rows; 128-row tiles; 256-row tiles
+    with staggered and with common starts of the contraction), 256-row tiles of weight gradients, and widths whose
+    gradient rows are whole 128-byte lines in both, one or neither type."""
+    announce("every kernel", n, k)
+    g = torch.Generator().manual_seed(n + k)
+    cs = torch.randint(0, 30, (128,), generator=g).tolist()
+    cs[3], cs[64], cs[127] = 0, 150, 290
+    off, cap = segments(cs, 16)
+    check_products_on_gpu(cs, n, k, off, cap, (1, 40 * 128, 120 * 128, 1 << 20), n + 2 * k)
+    # accumulating: fp32 sums that start at what is there, in rows that start inside a line
+    g = torch.Generator(device=DEV).manual_seed(7)
+    rn = lambda *sh: torch.randn(sh, generator=g, device=DEV)
+    a, dy, start = rn(cap, k).to(BF), (rn(cap, n) * 0.1).to(BF), rn(128, n, k)
+    dw = torch.empty(128 * n * k + 4, device=DEV)[4:].view(128, n, k).copy_(start)   # 16 bytes past a line
+    moe.moe_grouped_gemm_bf16_wgrad(dy, a, i32(off), i32(cs), dw, 1, 0)
+    for e, c in enumerate(cs):
+        r = slice(off[e], off[e] + c)
+        ae, dt = a[r].double(), dy[r].double().T.contiguous()
+        mag = dt.abs() @ ae.abs() + start[e].double().abs()
+        err = (dw[e].double() - (dt @ ae + start[e].double())).abs()
+        assert (err <= ((c + 1) * 2.0 ** -23 * mag + TINY)).all(), e
+
+
 @pytest.mark.parametrize("n,k", [(65536, 8), (8, 65536), (72, 30000)])
 def test_products_widest(n, k):
     announce("widest", n, k)
