@@ -149,6 +149,8 @@ def check_arg(t, name: str, dtypes, shape=None, min_rows=None, optional=False):
         if shape is None:
             return
         got = t.shape
+        if got == shape and min_rows is None:
+            return
         if len(got) == len(shape):
             for g_, w_ in zip(got, shape):
                 if w_ is not None and g_ != w_:
@@ -187,11 +189,14 @@ def check_device(*tensors):
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        device = t.get_device()   # -1 on the CPU
+        if device == current:
+            continue
+        if device < 0:
             raise ValueError(f"a tensor is on {t.device}; the library needs tensors on the current CUDA device")
         if current is None:
             current = torch.cuda.current_device()
-        if t.get_device() != current:
+        if device != current:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{current}")
 
 
