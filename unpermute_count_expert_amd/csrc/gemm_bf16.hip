@@ -316,8 +316,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     // its blocks share operands in its L2.  Where tiles cost alike: the XCD's
     // eighth of the sequence.  Where they do not: of every round of gridDim.x
     // tiles the XCD's eighth, so that each has its share of the long ones
-    // (4096 tokens on hot experts, 2048 x 768: 207-235 -> 168 us; 512 tokens,
-    // all short, fp32: 262 us dealt, 246 in eighths).
+    // (4096 tokens on hot experts, 2048 x 768: 363 us in eighths, 165 dealt; 512
+    // tokens, all short, 1536 x 2048, fp32: 253 and 263).
     const int ntn = (N + BN - 1) / BN;
     const int xcd = blockIdx.x & 7, nslots = gridDim.x >> 3;
     const int64_t total = (int64_t)mtiles * ntn;
@@ -575,8 +575,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     // A gradient's bytes are most of a short batch's time.  There (kLines) the
     // lanes eight apart trade halves of two neighbouring pieces, so that a
     // store writes eight rows of whole 128-byte lines instead of sixteen of
-    // half lines (512 tokens, 1536 x 2048: fp32 gradients 290 -> 245 us, bf16
-    // 234 -> 149; forward and dgrad are level or 3% slower with it), and
+    // half lines (512 tokens, 1536 x 2048: fp32 gradients 437 -> 253 us, bf16
+    // 224 -> 148; forward and dgrad are level or 2% slower with it), and
     // non-temporal where the rows are whole lines (4096 tokens on hot experts,
     // 2048 x 768, bf16: 150 us, plainly 202).  Where they are not, a piece's
     // two half-filled lines have to meet their other halves in L2: plain
