@@ -72,7 +72,8 @@ class MoeLayer:
 
 @dataclass
 class SavedRows:
-    """What MoeTrainLayer.backward needs of one forward call."""
+    """What MoeTrainLayer.backward needs of one forward call.  topk_weights is the caller's own tensor: it and the
+    layer's weights stay as they are until then."""
     tokens: int
     topk_weights: torch.Tensor
     counts: torch.Tensor
