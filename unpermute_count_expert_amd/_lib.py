@@ -15,6 +15,11 @@ from typing import Optional
 
 import torch
 
+try:
+    from . import _host
+except ImportError:   # not built
+    _host = None
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_hip.so")
 
@@ -120,13 +125,16 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 # A call on a few tokens takes the GPU less time than it takes the host to
-# check and pass the arguments (measured per call with five tensors: 13.8 us,
-# of which the library's own part 4.2), so these helpers stay lean: the
-# current stream's handle without building a Stream object (2.9 -> 0.3 us),
-# the current device asked once a call (2.8 -> 0.6 us).
+# check and pass the arguments, so the helpers below stay lean: the current
+# stream's handle without building a Stream object (2.9 -> 0.2 us), the
+# current device asked once a call (2.8 -> 0.6 us), and, where csrc/
+# host_checks.cpp is built, the checks of plain tensors that fit answered
+# natively (bound below; a SiLU-mul call 7.0 -> 4.5 us, 97 gradients with
+# outputs 50 -> 1.5 us).  These functions are the checks: they run without it,
+# and for whatever it does not answer.
 def _stream(stream=None):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # after check_device: there is one
     return stream.cuda_stream
 
 
@@ -198,6 +206,12 @@ def check_device(*tensors):
             current = torch.cuda.current_device()
         if device != current:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{current}")
+
+
+PYTHON_CHECKS = check_arg, check_device, _ptr
+if _host is not None:
+    _host.bind(*PYTHON_CHECKS)
+    check_arg, check_device, _ptr = _host.check_arg, _host.check_device, _host.ptr
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -670,6 +684,10 @@ def _check_grads(ts, what):
 
 def _grad_list(grads, outs):
     """The moe_grad_tensor array (four 64-bit words a tensor: grad, out, numel, dtype) of a list of tensors."""
+    if _host is not None:
+        words = _host.grad_words(grads, outs)
+        if words is not None:
+            return words
     kinds = _check_grads(grads, "gradient")
     sizes = list(map(torch.Tensor.numel, grads))
     words = [0] * (4 * len(grads))
@@ -684,7 +702,7 @@ def _grad_list(grads, outs):
         if _check_grads(outs, "out") != kinds or list(map(torch.Tensor.numel, outs)) != sizes:
             raise ValueError("an out has another dtype or number of elements than its gradient")
         words[1::4] = map(torch.Tensor.data_ptr, outs)
-    return array.array("Q", words)
+    return array.array("Q", words).tobytes()
 
 
 def moe_grad_workspace_size(num_tensors: int) -> int:
@@ -700,7 +718,7 @@ def moe_grad_sumsq(grads, sumsq, workspace, stream=None):
     check_arg(workspace, "workspace", (torch.uint8, torch.int32, torch.float64))
     table = _grad_list(grads, grads)
     check_device(sumsq, workspace)
-    _check(load().moe_grad_sumsq(table.buffer_info()[0], len(grads), _ptr(sumsq), _ptr(workspace),
+    _check(load().moe_grad_sumsq(table, len(grads), _ptr(sumsq), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)), "moe_grad_sumsq")
 
 
@@ -713,5 +731,5 @@ def moe_grad_clip(grads, outs, sumsq, max_norm, norm=None, stream=None):
     check_arg(norm, "norm", F32, (1,), optional=True)
     table = _grad_list(grads, outs)
     check_device(sumsq, norm)
-    _check(load().moe_grad_clip(table.buffer_info()[0], len(grads), _ptr(sumsq), max_norm, _ptr(norm),
+    _check(load().moe_grad_clip(table, len(grads), _ptr(sumsq), max_norm, _ptr(norm),
                                 _stream(stream)), "moe_grad_clip")

@@ -1,12 +1,14 @@
-"""Compiles the gfx950 HIP library libmoe_hip.so in-tree with hipcc."""
+"""Compiles the gfx950 HIP library libmoe_hip.so and the binding's native argument checks (_host.so) in-tree."""
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmoe_hip.so")
+HOST = os.path.join(PKG, "_host.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -30,7 +32,25 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(LIB + ".tmp", LIB)
+    build_host(verbose)
     return LIB
+
+
+def build_host(verbose: bool = False) -> str:
+    """csrc/host_checks.cpp: host code only, against torch's headers."""
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in cpp_extension.include_paths()), f"-I{sysconfig.get_paths()['include']}",
+           os.path.join(PKG, "csrc", "host_checks.cpp"), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-o", HOST + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(HOST + ".tmp", HOST)
+    return HOST
 
 
 if __name__ == "__main__":
