@@ -423,7 +423,7 @@ def flat_views(sizes, skew, g, scale=1.0):
     return out
 
 
-@pytest.mark.parametrize("sizes", [[1], [0, 3, 0], [7, 8, 9, 15, 16, 17], [4097, 1, 100000, 8191],
+@pytest.mark.parametrize("sizes", [[1], [0, 3, 0], [5000, 0, 9], [7, 8, 9, 15, 16, 17], [4097, 1, 100000, 8191],
                                    [5] * 200, [3_000_001, 17], []])
 @pytest.mark.parametrize("skew", [0, 1, 3])
 @pytest.mark.parametrize("max_norm", [0.0, 0.5, 1e9])
