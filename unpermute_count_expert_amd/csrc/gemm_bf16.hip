@@ -93,16 +93,31 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef __attribute__((address_space(3))) const v8bf* lds_v8;
 typedef __attribute__((address_space(3))) v4s* lds_v4;
 
-// rows [lo, hi) of expert e, cut at the next segment and at cap_rows
-__device__ __forceinline__ void segment(const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts,
-                                        int64_t cap_rows, int e, int& lo, int& hi) {
-    const int64_t next = offsets[e + 1];
+// rows [lo, hi) of an expert's segment, cut at the next one and at cap_rows
+__device__ __forceinline__ void cut(int offset, int next_offset, int count, int64_t cap_rows, int& lo, int& hi) {
+    const int64_t next = next_offset;
     const int64_t end = next < 0 ? 0 : (next < cap_rows ? next : cap_rows);
-    int64_t l = offsets[e];
+    int64_t l = offset;
     l = l < 0 ? 0 : (l > end ? end : l);
-    const int64_t c = counts[e] < 0 ? 0 : counts[e];
+    const int64_t c = count < 0 ? 0 : count;
     lo = (int)l;
     hi = (int)(l + c < end ? l + c : end);
+}
+__device__ __forceinline__ void segment(const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts,
+                                        int64_t cap_rows, int e, int& lo, int& hi) {
+    cut(offsets[e], offsets[e + 1], counts[e], cap_rows, lo, hi);
+}
+// the segments of experts 2 t and 2 t + 1, no rows past El; loaded without
+// conditions, so together
+__device__ __forceinline__ void segments(const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts,
+                                         int64_t cap_rows, int El, int t, int (&lo)[2], int (&hi)[2]) {
+    int off[3], num[2];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) off[j] = offsets[min(2 * t + j, El)];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) num[j] = counts[min(2 * t + j, El - 1)];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) cut(off[j], off[j + 1], 2 * t + j < El ? num[j] : 0, cap_rows, lo[j], hi[j]);
 }
 
 // Exclusive prefix over the experts of nt (two consecutive experts a thread)
@@ -244,15 +259,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     int* s_lo = s_tab + El;
     int* s_hi = s_lo + El;
     const int ntm_w = (n_out + BM - 1) / BM;   // wgrad: m-tiles of every expert
-    int lo[2], hi[2], nt[2] = {0, 0};
+    int lo[2], hi[2], nt[2];
+    segments(offsets, counts, cap_rows, El, tid, lo, hi);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int e = tid * 2 + j;
-        if (e < El) {
-            segment(offsets, counts, cap_rows, e, lo[j], hi[j]);
-            nt[j] = (hi[j] - lo[j] + BM - 1) / BM;
-        }
-    }
+    for (int j = 0; j < 2; ++j) nt[j] = (hi[j] - lo[j] + BM - 1) / BM;
     int mtiles;
     bool alike = true;
     if constexpr (MODE == kWgrad) {
@@ -733,17 +743,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int uw = wave >> 2, kw = wave & 3;
     const int N = MODE == kFwd ? n_out : k_in, C = MODE == kFwd ? k_in : n_out;
-    int nt[2];
+    int lo2[2], hi2[2], nt[2];
+    segments(offsets, counts, cap_rows, El, tid, lo2, hi2);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int e = tid * 2 + j;
-        nt[j] = 0;
-        if (e < El) {
-            int lo, hi;
-            segment(offsets, counts, cap_rows, e, lo, hi);
-            nt[j] = (hi - lo + 15) / 16;
-        }
-    }
+    for (int j = 0; j < 2; ++j) nt[j] = (hi2[j] - lo2[j] + 15) / 16;
     const int tiles = expert_prefix(nt, El, cap_rows / 16 + El, s_tpre, reinterpret_cast<int64_t*>(smem));
     const int ncu = (N + NC - 1) / NC;
     const int64_t units = (int64_t)tiles * ncu;
