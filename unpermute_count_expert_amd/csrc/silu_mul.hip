@@ -40,19 +40,19 @@ __global__ __launch_bounds__(kThreads) void k_silu(const uint16_t* h, const uint
     if (offsets != nullptr) {
         // 64-bit sums, stored capped at `rows`: segments that overlap (offsets
         // out of order) cannot push the walk past its tables
-        int64_t c[kPer], sum = 0;
+        int64_t sum = 0;
+        int c[kPer], off[kPer + 1], num[kPer];   // loaded without conditions, so together
+        const int rows32 = (int)rows;
+#pragma unroll
+        for (int j = 0; j <= kPer; ++j) off[j] = offsets[min((int)threadIdx.x * kPer + j, El)];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) num[j] = counts[min((int)threadIdx.x * kPer + j, El - 1)];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int e = threadIdx.x * kPer + j;
-            c[j] = 0;
-            if (e < El) {
-                const int64_t next = offsets[e + 1], end = next < 0 ? 0 : (next < rows ? next : rows);
-                int64_t lo = offsets[e];
-                lo = lo < 0 ? 0 : (lo > end ? end : lo);
-                const int64_t cnt = counts[e] < 0 ? 0 : counts[e];
-                c[j] = lo + cnt < end ? cnt : end - lo;
-                s_lo[e] = (int)lo;
-            }
+            const int end = max(0, min(off[j + 1], rows32)), lo = max(0, min(off[j], end));
+            c[j] = e < El ? min(max(num[j], 0), end - lo) : 0;
+            if (e < El) s_lo[e] = lo;
             sum += c[j];
         }
         const int64_t incl = wave_inclusive_scan(sum);
@@ -71,20 +71,21 @@ __global__ __launch_bounds__(kThreads) void k_silu(const uint16_t* h, const uint
         __syncthreads();
         total = s_pre[El];
     }
-    const int64_t v_lo = total * blockIdx.x / gridDim.x, v_hi = total * (blockIdx.x + 1) / gridDim.x;
+    // the block's rows: total / grid of them, the first total mod grid blocks one more
+    const uint32_t per = (uint32_t)total / gridDim.x, more = (uint32_t)total - per * gridDim.x;
+    const int64_t v_lo = (int64_t)(blockIdx.x * per + min(blockIdx.x, more));
+    const int64_t v_hi = v_lo + per + (blockIdx.x < more);
     if (v_lo >= v_hi) return;
     const int nch = n / 8;
     const int step_r = kThreads / nch, step_c = kThreads - step_r * nch;
     int64_t v = v_lo + threadIdx.x / nch;
     int c = threadIdx.x % nch;
     int e = 0;
-    if (offsets != nullptr && v < v_hi) {
-        int lo = 0, hi = El - 1;   // the last expert with s_pre[e] <= v
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_pre[mid] <= v) lo = mid; else hi = mid - 1;
-        }
-        e = lo;
+    if (offsets != nullptr) {
+        // the last expert with s_pre[e] <= the block's first row; the walk goes on from there
+        const int lane = threadIdx.x & (kWave - 1);
+        e = -1;
+        for (int j = 0; j < El; j += kWave) e += __popcll(ballot(j + lane < El && s_pre[min(j + lane, El)] <= v_lo));
     }
     for (; v < v_hi;) {
         int64_t r = v;
@@ -122,14 +123,17 @@ __global__ __launch_bounds__(kThreads) void k_silu(const uint16_t* h, const uint
     }
 }
 
-// One chunk a thread until there are 64 blocks per CU, then more.  131072 rows
-// of 768, forward / backward: 8 blocks per CU 119 / 197 us, 32 107 / 183, 64
-// 106 / 171 (5.7 / 5.9 TB/s), 128 116 / 170, 256 157 / 185: many short
+// Two chunks a thread of the buffer's rows (which of them are valid the host
+// does not know) until there are 128 blocks per CU, then more: many short
 // blocks keep the streams' pages close together, until every block's scan of
-// the counts tells.
+// the counts tells.  131072 valid rows of 147328, 768 wide, forward / backward
+// us: 32 blocks per CU 105 / 181, 64 97 / 170, 128 92 / 161, 192 111 / 156;
+// 16000 valid rows of 32256: one chunk a thread 24 / 27, two 16.5 / 22, three
+// 14.6 / 23, six 14.5 / 23; 128 of 4096: 3.6 / 3.7 and 3.05 / 3.4; 1400 of
+// 1520, 1504 wide: 5.1 / 6.2, 4.8 / 6.5 and 5.6 / 7.1.
 unsigned grid_for(int64_t rows, int n, int num_cus) {
-    int64_t b = (rows * (n / 8) + kThreads - 1) / kThreads;
-    b = b > 64 * num_cus ? 64 * num_cus : b;
+    int64_t b = (rows * (n / 8) + 2 * kThreads - 1) / (2 * kThreads);
+    b = b > 128 * num_cus ? 128 * num_cus : b;
     return (unsigned)(b < 1 ? 1 : b);
 }
 
