@@ -51,7 +51,9 @@
 //    for their weights), waits that count the stores in flight instead of
 //    letting them drain (level), the last round's tiles in quarters where
 //    those fill it (8 experts of 4096 x 4096: 3-9% faster; 128 experts, 8192
-//    and more tokens: level to 3% slower).
+//    and more tokens: level to 3% slower), a weight gradient's finished tile
+//    kept in registers and stored a row block a step (128-row tiles, 5-45%
+//    slower: stores go fastest all at once).
 //  * The weight-side fragment is the MFMA's first operand, so a lane holds
 //    four consecutive columns of one row; for bf16 two column blocks are
 //    exchanged between neighbouring 16-lane rows (v_permlane16_swap) to 16
