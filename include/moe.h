@@ -391,7 +391,7 @@ int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int
  *   dw[e,n,k] = sum over e's valid rows r of dy[r,n] * a[r,k]
  * (0 for an expert without rows), in fp32 or rounded once to bf16
  * (dw_dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16).  accumulate = 1 (fp32 only)
- * adds it to what dw holds, which is where the fp32 sum then starts.
+ * adds the finished sum to what dw holds, one more rounding.
  * dy [cap_rows,n_out], a [cap_rows,k_in] bf16, dw [El,n_out,k_in]; dw
  * overlaps neither input. */
 #define MOE_DTYPE_BF16 0

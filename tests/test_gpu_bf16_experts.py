@@ -761,3 +761,30 @@ def test_clip_many_tensors_in_a_graph():
         for t, o in zip(grads, outs):
             want = t.double() * c
             assert ((o.double() - want).abs() <= 5 * 2.0 ** -24 * want.abs()).all()
+
+
+@pytest.mark.parametrize("experts,n,k", [(5, 72, 136), (5, 72, 128), (128, 512, 40), (128, 512, 64)])
+def test_wgrad_adds_its_finished_sum(experts, n, k):
+    """accumulate rounds once, however many rows an expert has: the rows are small integers, so that every order of
+    their sum is exact, and start + sum needs more bits than fp32 has (start: multiples of 2^-20 below 2^3; sums: up
+    to some hundreds) but no more than fp64, which rounds to the one fp32 answer.  128-row and 256-row tiles, rows of
+    whole 128-byte lines and not."""
+    announce("wgrad accumulated", experts, n, k)
+    g = torch.Generator().manual_seed(experts + n + k)
+    cs = [1300, 0, 1, 64, 700] + torch.randint(0, 200, (experts - 5,), generator=g).tolist()
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g).to(BF)
+    a, dy = ints(cap, k), ints(cap, n)
+    start = (torch.randint(-2 ** 23, 2 ** 23, (experts, n, k), generator=g).double() * 2.0 ** -20).float()
+    A, D, dw = poison(a, mask).to(DEV), poison(dy, mask).to(DEV), start.to(DEV)
+    want, rounded = start.clone(), 0
+    for _ in range(3):
+        moe.moe_grouped_gemm_bf16_wgrad(D, A, i32(off), i32(cs), dw, 1, 0)
+        for e, c in enumerate(cs):
+            r = slice(off[e], off[e] + c)
+            exact = want[e].double() + dy[r].double().T.contiguous() @ a[r].double()
+            want[e] = exact.float()
+            rounded += int((want[e].double() != exact).sum())
+        assert torch.equal(dw.cpu(), want)
+    assert rounded > n * k

@@ -607,16 +607,43 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         else
             __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
     };
+    // ACC adds what is there to the finished sums, one rounding at its magnitude
+    // (starting the sums at it would round at it every 32 rows).  It is read
+    // in the stores' own pieces, kOld row blocks ahead of its use: the step's
+    // fragments are dead here and leave the registers.  Bound by its bytes, 8 an
+    // element (4096 tokens, 1536 x 2048: 606 us, 5.6 TB/s; one, two and four
+    // blocks ahead: 627, 620, 606), non-temporal as the stores are (read
+    // plainly 678; 725 tokens, 704 x 1256, whose rows are not whole lines: 204,
+    // non-temporal 233).
+    constexpr int kOld = 4;
+    auto get16 = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t at) __attribute__((always_inline)) {
+        return __builtin_bit_cast(v4f, whole ? __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kNonTemporal)
+                                             : __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+    };
     auto store = [&]() __attribute__((always_inline)) {
         if (!done.mine) return;
         constexpr bool kLines = MODE == kWgrad;
+        static_assert(!ACC || (kLines && F32), "accumulating: fp32 weight gradients");
         const Rows x = rows_of(done);
         const bool up = kLines && (lane & 8);
         const int c1 = c0 + (up ? kCols : 0);
         const uint32_t v = (uint32_t)(((lane & (kLines ? 7 : 15)) * N + c1) * ES);
         auto at = [&](int p) __attribute__((always_inline)) { return c1 + kCols * p < x.w ? v + kCols * ES * p : kNowhere; };
+        v4f old[ACC ? MI : 1][ACC ? kPieces : 1];
+        auto fetch = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int p = 0; p < kPieces; p += 2)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) old[i][p + h] = get16(from_row(x, 16 * i + 8 * h), at(p));
+        };
+        if constexpr (ACC) {
+#pragma unroll
+            for (int i = 0; i < kOld; ++i) fetch(i);
+        }
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
+            if constexpr (ACC)
+                if (i + kOld < MI) fetch(i + kOld);
 #pragma unroll
             for (int p = 0; p < kPieces; p += 2) {
                 v4u lo, hi;
@@ -634,6 +661,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
                         lo[q] = up ? got : lo[q];
                         hi[q] = up ? hi[q] : got;
                     }
+                    if constexpr (ACC) {
+                        lo = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, lo) + old[i][p]);
+                        hi = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, hi) + old[i][p + 1]);
+                    }
                     put16(lo, from_row(x, 16 * i), at(p));
                     put16(hi, from_row(x, 16 * i + 8), at(p));
                 } else {
@@ -644,26 +675,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
             sched_fence();
         }
     };
-    // The sums' start: zero, or what is there (ACC).  Adding it at the end
-    // instead would save the sums' roundings at its magnitude (2^-24 of it a
-    // step) but needs registers that the fragments hold.
-    auto begin = [&](const Part& t) __attribute__((always_inline)) {
-        if constexpr (ACC) {
-            if (!t.mine) return;
-            const Rows x = rows_of(t);
-            const uint32_t v = (uint32_t)(((lane & 15) * N + c0) * ES);
+    auto begin = [&]() __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int p = 0; p < kPieces; ++p)
-                    acc[i][p] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
-                        from_row(x, 16 * i), c0 + kCols * p < x.w ? v + kCols * ES * p : kNowhere, 0, 0));
-        } else {
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+            for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     };
 
     // Before a group's reading phase, and before its multiplying phase: the
@@ -699,12 +715,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
                 if (have) store();
                 sched_fence();
                 done = t;
-                begin(t);
+                begin();
                 first = false;
                 have = true;
             }
             v8bf fa[2][MI], fb[2][NJ];   // the step's fragments: dead between steps, where the stores need registers
-            if (t.mine) load(fa, fb);
+            // (ACC: read whether they are used or not; else what the last step
+            // left would pass for them, and the registers are taken in store())
+            if (ACC || t.mine) load(fa, fb);
             if (!BT) puts();
             c_q = c_q + P >= kRing ? c_q + P - kRing : c_q + P;
             to_multiply();
