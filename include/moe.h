@@ -458,8 +458,9 @@ int moe_grad_sumsq(const moe_grad_tensor* tensors, int32_t num_tensors, double* 
                    size_t workspace_bytes, void* stream);
 
 /* out = g * c in the tensor's dtype (one rounding), with norm = sqrt(sumsq[0])
- * and c = min(1, max_norm / (norm + 1e-6)) (NaN where norm is NaN).  norm:
- * device float [1], 16-byte aligned, receives the norm before clipping (or
+ * and c = min(1, max_norm / (norm + 1e-6)) (NaN where norm is NaN), in fp64
+ * where fp32 does not hold them.  norm: device float [1], 16-byte aligned,
+ * receives the norm before clipping, infinity past the largest float (or
  * NULL).  max_norm >= 0.  An in-place tensor is not touched when c is 1. */
 int moe_grad_clip(const moe_grad_tensor* tensors, int32_t num_tensors, const double* sumsq, float max_norm,
                   float* norm, void* stream);

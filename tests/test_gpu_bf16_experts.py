@@ -788,3 +788,25 @@ def test_wgrad_adds_its_finished_sum(experts, n, k):
             rounded += int((want[e].double() != exact).sum())
         assert torch.equal(dw.cpu(), want)
     assert rounded > n * k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("value,max_norm", [(3e38, 1.0), (3e38, 1e30), (1e38, 1e-6), (1e30, 1.0), (1e30, 1e-30),
+                                            (1e-30, 1.0), (1e-30, 1e-32), (1e20, 0.0)])
+def test_clip_far_from_one(value, max_norm, dtype):
+    """Norms past the largest fp32 value and factors below the smallest: finite gradients come out as the formula
+    says.  The factor and the product are rounded to fp32 (2^-24 each; 2^-150 where the product is a denormal), then
+    the result to its type."""
+    announce("clip far from one", value, max_norm, dtype)
+    sign = torch.where(torch.rand(1003, generator=gen(1)) < 0.5, -1.0, 1.0)
+    before = (sign * value).to(dtype)
+    norm = float((before.double() ** 2).sum()) ** 0.5
+    want = before.double() * min(1.0, max_norm / (norm + 1e-6))
+    for skew in (0, 1):   # the output aligned as the gradient, and not
+        out = torch.full((1003 + 8,), 5.0, dtype=dtype, device=DEV)
+        s, nrm = clip([before.to(DEV)], [out[skew:skew + 1003]], max_norm)
+        assert abs(s - norm ** 2) <= 1e-12 * norm ** 2
+        assert nrm == float("inf") if norm > 3.41e38 else abs(nrm - norm) <= 2.0 ** -23 * norm
+        got = out[skew:skew + 1003].cpu().double()
+        tol = (2 * 2.0 ** -24 + EPS[dtype]) * want.abs() + 2.0 ** -149 + (TINY if dtype == BF else 0)
+        assert ((got - want).abs() <= tol * (1 + 2.0 ** -7)).all(), (skew, got[0], want[0])

@@ -153,21 +153,31 @@ __global__ __launch_bounds__(kThreads) void k_sum_partials(const double* __restr
 __global__ __launch_bounds__(kThreads) void k_clip(List L, const double* __restrict__ sumsq, float max_norm,
                                                    float* __restrict__ norm) {
     const Firsts firsts = firsts_of(L);
-    const float nrm = (float)__builtin_sqrt(sumsq[0]);
+    // The norm of finite gradients may lie past the largest fp32 value and the
+    // factor below the smallest normal one: the factor is fp64, and where it is
+    // that small the products are, too.
+    const double root = __builtin_sqrt(sumsq[0]);
+    const float nrm = (float)root;
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = nrm;
-    const float ratio = max_norm / (nrm + 1e-6f);
-    const float c = ratio >= 1.0f ? 1.0f : ratio;   // a NaN ratio stays NaN
+    double c64 = 1.0;
+    if (!(nrm + 1e-6f <= max_norm && nrm < HUGE_VALF)) {
+        const double ratio = max_norm / (root + 1e-6);
+        c64 = ratio >= 1.0 ? 1.0 : ratio;   // a NaN ratio stays NaN
+    }
+    const float c = (float)c64;
+    const bool wide = c64 > 0.0 && c64 < 0x1p-126;
     for (int64_t q = blockIdx.x; q < L.first[L.num]; q += gridDim.x) {
         const Item it = item_of<kClipChunk>(L, firsts, L.first[L.num] - 1 - q);
         const uintptr_t o = reinterpret_cast<uintptr_t>(L.out[it.i]);
         if (o == it.g && c == 1.0f) continue;
         const bool f32 = it.es == 4;
         auto one = [&](uintptr_t p) {
-            const float v = load_el(p, it.es) * c;
+            const float x = load_el(p, it.es);
+            const float v = wide ? (float)(x * c64) : x * c;
             if (f32) *reinterpret_cast<float*>(o + (p - it.g)) = v;
             else *reinterpret_cast<uint16_t*>(o + (p - it.g)) = f32_to_bf16(v);
         };
-        if (((o - it.g) & (kVec - 1)) != 0) {   // the two are not aligned alike
+        if (wide || ((o - it.g) & (kVec - 1)) != 0) {   // or the two are not aligned alike
             for (uintptr_t p = it.lo + threadIdx.x * it.es; p < it.hi; p += kThreads * it.es) one(p);
             continue;
         }
