@@ -452,6 +452,7 @@ int moe_grad_workspace_size(int32_t num_tensors, size_t* bytes);
 /* sumsq[0] = sum over all tensors and elements of g^2, in fp64 (squares and
  * sums: no fp32 value overflows or vanishes), in an order fixed by the list,
  * so equal calls give equal bits.  sumsq: device double, 16-byte aligned.
+ * Neither it nor the workspace's needed bytes overlap a gradient.
  * Ranks that hold parts of the parameters all-reduce (sum) it before
  * moe_grad_clip. */
 int moe_grad_sumsq(const moe_grad_tensor* tensors, int32_t num_tensors, double* sumsq, void* workspace,

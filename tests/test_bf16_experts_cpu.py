@@ -152,6 +152,17 @@ def test_clip_refuses_overlapping_memory():
     assert clip((G, G, 100, 1, 0), norm=C.c_void_p(G + 16)) == ARG             # the norm in a tensor
 
 
+def test_sumsq_refuses_to_write_over_a_gradient():
+    need = moe.moe_grad_workspace_size(1)
+    at = lambda p: C.c_void_p(p)
+    inside = (G, None, 100, 1, 0)   # 400 bytes
+    assert sumsq(inside, out=at(G)) == ARG and sumsq(inside, out=at(G + 384)) == ARG
+    assert sumsq((G + 4, None, 1, 1, 0), out=at(G)) == ARG                       # the double's second half
+    assert sumsq(inside, ws=at(G)) == ARG and sumsq(inside, ws=at(G + 384)) == ARG
+    assert sumsq(inside, ws=at(G - need + 16)) == ARG                            # the workspace's last bytes
+    assert sumsq((3 * G, None, 5, 0, 0), inside, ws=at(G - need + 16)) == ARG    # any tensor of the list
+
+
 def test_workspace_size():
     assert moe.moe_grad_workspace_size(0) == moe.moe_grad_workspace_size(1) > 0
     assert moe.moe_grad_workspace_size(1000) > moe.moe_grad_workspace_size(100)

@@ -810,3 +810,17 @@ def test_clip_far_from_one(value, max_norm, dtype):
         got = out[skew:skew + 1003].cpu().double()
         tol = (2 * 2.0 ** -24 + EPS[dtype]) * want.abs() + 2.0 ** -149 + (TINY if dtype == BF else 0)
         assert ((got - want).abs() <= tol * (1 + 2.0 ** -7)).all(), (skew, got[0], want[0])
+
+
+def test_clip_in_one_buffer():
+    """Workspace, sum and gradients side by side, with the workspace longer than what is needed."""
+    need = moe.moe_grad_workspace_size(2)
+    buf = torch.zeros(need + 16 + 4 * 3000, dtype=torch.uint8, device=DEV)
+    ws, s, flat = buf[:need], buf[need:need + 8].view(F64), buf[need + 16:].view(F32)
+    flat.copy_(torch.arange(3000) % 7 - 3)
+    grads, before = [flat[:1111], flat[1111:]], flat.clone()
+    moe.moe_grad_sumsq(grads, s, ws)
+    assert float(s) == float((before.double() ** 2).sum()) and torch.equal(flat, before)
+    s.zero_()
+    moe.moe_grad_sumsq(grads[:1], s, buf[-16 - need:].clone())   # another workspace, any contents
+    assert float(s) == float((before[:1111].double() ** 2).sum())

@@ -1214,6 +1214,12 @@ int moe_grad_sumsq(const moe_grad_tensor* tensors, int32_t num_tensors, double* 
     REQUIRE_PTR(workspace);
     const size_t need = moe::grad_workspace(num_tensors > 0 ? num_tensors : 1);
     REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+    for (int32_t i = 0; i < num_tensors; ++i) {
+        const size_t bytes = (size_t)tensors[i].numel * (tensors[i].dtype == MOE_DTYPE_F32 ? 4 : 2);
+        REQUIRE(!overlaps(tensors[i].grad, bytes, workspace, need) &&
+                    !overlaps(tensors[i].grad, bytes, sumsq, sizeof(double)),
+                MOE_ERR_INVALID_ARG, "tensor %d: the workspace or sumsq overlaps its grad", i);
+    }
     st = check_device(nullptr);
     if (st) return st;
     HIP_OK(moe::launch_grad_sumsq(tensors, num_tensors, sumsq, static_cast<double*>(workspace),
