@@ -1,10 +1,12 @@
 """The binding's native argument checks answer as the Python functions do: the
 same calls pass, the others raise the same error."""
+import subprocess
+
 import pytest
 import torch
 
 import unpermute_count_expert_amd as moe
-from unpermute_count_expert_amd import _lib
+from unpermute_count_expert_amd import _lib, build
 
 BF = torch.bfloat16
 py_arg, py_device, py_ptr = _lib.PYTHON_CHECKS
@@ -97,3 +99,32 @@ def test_on_the_gpu(monkeypatch):
     for (g, o), got in zip(lists, native):
         assert got == outcome(_lib._grad_list, g, g if g is o else o)
     assert isinstance(native[0], bytes) and isinstance(native[1], bytes) and native[2][0] is ValueError
+
+
+@pytest.mark.parametrize("error", [FileNotFoundError("no compiler"), subprocess.CalledProcessError(1, "c++"),
+                                   ImportError("no torch headers")])
+def test_build_without_the_native_checks(monkeypatch, tmp_path, capfd, error):
+    """Where the module cannot be built the library still is, and a module of older sources is not left behind."""
+    lib, host = tmp_path / "lib.so", tmp_path / "host.so"
+    host.write_text("older")
+    monkeypatch.setattr(build, "LIB", str(lib))
+    monkeypatch.setattr(build, "HOST", str(host))
+    monkeypatch.setenv("CXX", "the-cxx")
+
+    def check_call(cmd):
+        if cmd[0] == "the-cxx":
+            raise error
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("library")
+
+    monkeypatch.setattr(subprocess, "check_call", check_call)
+    assert build.build() == str(lib)
+    assert lib.read_text() == "library" and not host.exists()
+    assert "argument checks" in capfd.readouterr().err
+
+
+def test_build_fails_without_the_library(monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(build, "HIPCC", str(tmp_path / "no-hipcc"))
+    with pytest.raises(FileNotFoundError):
+        build.build()
