@@ -824,3 +824,106 @@ def test_clip_in_one_buffer():
     s.zero_()
     moe.moe_grad_sumsq(grads[:1], s, buf[-16 - need:].clone())   # another workspace, any contents
     assert float(s) == float((before[:1111].double() ** 2).sum())
+
+
+# ---- the layer in a model that autograd trains ---------------------------------------------
+def explicit(layer, x, ids, tw, dout):
+    """Gradients through backward(), from zeroed sums: what autograd has to give."""
+    layer.zero_grad()
+    with torch.no_grad():
+        out, rows = layer.forward(x, ids, tw)
+        grads = layer.backward(dout, rows)
+    want = (out, *grads, layer.grad_w13.clone(), layer.grad_w2.clone())
+    layer.zero_grad()
+    return want
+
+
+@pytest.mark.parametrize("leaves", ["x", "tw", "w13", "w2", "x tw w13 w2"])
+def test_layer_through_autograd(leaves):
+    announce("layer autograd", leaves)
+    layer = make_layer(31)
+    x, ids, tw, dout = batch(32, 45)
+    want = explicit(layer, x, ids, tw, dout)
+    names = leaves.split()
+    x, tw = (t.clone().requires_grad_(n in names) for t, n in ((x, "x"), (tw, "tw")))
+    for n in ("w13", "w2"):
+        getattr(layer, n).requires_grad_(n in names)
+    # neither input is a leaf of the layer's own node, and the gradient arrives in another layout
+    out, rows = layer.forward(x * 1, ids, tw * 1)
+    assert out.requires_grad and torch.equal(out, want[0])
+    (out.t() * 1).backward(dout.t().contiguous())
+    got = (out, x.grad, tw.grad, layer.grad_w13, layer.grad_w2)
+    for a, b, n in zip(got, want, ("out", "x", "tw", "w13", "w2")):
+        assert torch.equal(a, b) if a is not None else n not in names, n
+    assert layer.w13.grad is None and layer.w2.grad is None
+    # backward() on the same rows adds once more
+    dx, dtw = layer.backward(dout, rows)
+    assert torch.equal(dx, want[1]) and torch.equal(dtw, want[2]) and not torch.equal(layer.grad_w2, want[4])
+
+
+def test_layers_chained_through_autograd():
+    first, second = make_layer(33), make_layer(34)
+    x, ids, tw, dout = batch(35, 30)
+    h, r1 = first.forward(x, ids, tw)
+    _, r2 = second.forward(h, ids, tw)
+    dh, _ = second.backward(dout, r2)
+    dx, _ = first.backward(dh, r1)
+    want = [t.clone() for t in (dx, first.grad_w13, first.grad_w2, second.grad_w13, second.grad_w2)]
+    first.zero_grad(), second.zero_grad()
+    x.requires_grad_()
+    second.forward(first.forward(x, ids, tw)[0], ids, tw)[0].backward(dout)
+    for a, b in zip((x.grad, first.grad_w13, first.grad_w2, second.grad_w13, second.grad_w2), want):
+        assert torch.equal(a, b)
+
+
+def test_layer_without_gradients_has_no_graph():
+    layer = make_layer(36)
+    x, ids, tw, dout = batch(37, 9)
+    assert not layer.forward(x, ids, tw)[0].requires_grad
+    x.requires_grad_()
+    layer.w2.requires_grad_()
+    with torch.no_grad():
+        assert not layer.forward(x, ids, tw)[0].requires_grad
+
+
+@pytest.mark.parametrize("what", ["w13", "w2", "tw"])
+def test_layer_refuses_weights_changed_before_the_backward(what):
+    layer = make_layer(38)
+    x, ids, tw, dout = batch(39, 9)
+    out, _ = layer.forward(x.requires_grad_(), ids, tw)
+    (tw if what == "tw" else getattr(layer, what)).mul_(0.5)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.backward(dout)
+
+
+def test_layer_autograd_in_a_graph():
+    """Forward and autograd's backward captured while an eager graph of the same layer lives, replayed on new inputs."""
+    layer, eager = make_layer(40), make_layer(40)
+    layer.w13.requires_grad_()
+    x, ids, tw, dout = batch(41, 33)
+    alive = layer.forward(x, ids, tw)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        layer.zero_grad()
+        out, _ = layer.forward(x, ids, tw)
+        out.backward(dout)
+        return out.detach()
+
+    with torch.cuda.stream(st):
+        step()
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (42, 43, 44):
+        new = batch(seed, 33)
+        for dst, src in zip((x, ids, tw, dout), new):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = explicit(eager, *new)
+        for a, b in zip((got, layer.grad_w13, layer.grad_w2), (want[0], want[3], want[4])):
+            assert torch.equal(a, b), seed
+    assert alive[0].requires_grad

@@ -96,6 +96,12 @@ class MoeTrainLayer:
     expert weights to the fp32 grad_w13 / grad_w2 (zero_grad() clears them);
     clip_gradients() scales them in place to a global norm.  Every step is a
     library call on the current stream.  N and K: multiples of 128.
+
+    With gradients enabled and any of tokens, router weights and expert
+    weights requiring them, forward()'s output carries a graph whose backward
+    is backward(): the tokens and router weights get their gradients through
+    autograd.  The expert weights' are in grad_w13 / grad_w2 alike (their own
+    .grad stays as it is: it would hold a bf16 sum).
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, num_global_experts: int,
@@ -131,9 +137,16 @@ class MoeTrainLayer:
         """(out [M, K] bf16, the rows backward() needs)."""
         _lib.check_arg(x, "x", (torch.bfloat16,), (None, self.K))
         _lib.check_arg(topk_ids, "topk_ids", _lib.I32, (x.shape[0], None))
-        M, topk = topk_ids.shape
-        _lib.check_arg(topk_weights, "topk_weights", _lib.F32, (M, topk))
+        _lib.check_arg(topk_weights, "topk_weights", _lib.F32, topk_ids.shape)
         _lib.check_device(x, topk_ids, topk_weights, self.w13)
+        if torch.is_grad_enabled():
+            weights = self.w13.requires_grad or self.w2.requires_grad
+            if weights or x.requires_grad or topk_weights.requires_grad:
+                return _Graph.apply(x, topk_weights, _anchor() if weights else None, topk_ids, self)
+        return self._forward(x, topk_ids, topk_weights)
+
+    def _forward(self, x, topk_ids, topk_weights):
+        M, topk = topk_ids.shape
         El, K, N, i32 = self.El, self.K, self.N, torch.int32
         cap = _lib.moe_max_rows(M, topk, El, self.align)
         s = SavedRows(M, topk_weights, self._empty(El, dtype=i32), self._empty(El + 1, dtype=i32),
@@ -180,3 +193,29 @@ class MoeTrainLayer:
             reduce(sumsq)
         _lib.moe_grad_clip(grads, None, sumsq, max_norm, norm)
         return norm
+
+
+def _anchor() -> torch.Tensor:
+    """What makes the output require a gradient for the expert weights.  They are no inputs of the graph, as nothing
+    goes to their .grad; a new leaf a call also keeps graphs of one layer apart (a captured backward must share no
+    leaf with an eager graph that lives)."""
+    return torch.empty(0, requires_grad=True)
+
+
+class _Graph(torch.autograd.Function):
+    """MoeTrainLayer.forward and backward as one node.  What backward reads besides the rows is saved with its
+    version, so that weights changed in between are an error."""
+
+    @staticmethod
+    def forward(ctx, x, topk_weights, anchor, topk_ids, layer):
+        out, ctx.rows = layer._forward(x, topk_ids, topk_weights)
+        ctx.layer = layer
+        ctx.save_for_backward(topk_weights, layer.w13.detach(), layer.w2.detach())
+        return out, ctx.rows
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, _):
+        ctx.saved_tensors   # the check of their versions
+        dx, dweights = ctx.layer.backward(dout.contiguous(), ctx.rows)
+        return dx, dweights, None, None, None
