@@ -358,9 +358,11 @@ int moe_experts_batched_masked(const uint8_t* a_q, const float* a_s, const int32
  * once.
  *
  * rows_hint (the products): about how many rows are valid in all, Mc * topk
- * for instance; <= 0 means cap_rows.  It picks the tile shape, so it changes
- * the speed, and the order of the fp32 sums with it, but any value is
- * correct. */
+ * for instance; <= 0 means cap_rows.  In the product and its gradient by the
+ * rows it picks the tile shape, so it changes the speed, and the order of the
+ * fp32 sums with it, but any value is correct.  The gradient by the weights
+ * has whole matrices as outputs: its tiles go by their sizes alone, and it
+ * does not read the hint. */
 
 /* moe_permute for bf16 rows: x [Mc,K] bf16, a_perm [cap_rows,K] bf16;
  * a_perm[row] = x[t] with the rows, counts, expert_offsets, inv_perm and

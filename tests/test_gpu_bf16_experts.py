@@ -927,3 +927,16 @@ def test_layer_autograd_in_a_graph():
         for a, b in zip((got, layer.grad_w13, layer.grad_w2), (want[0], want[3], want[4])):
             assert torch.equal(a, b), seed
     assert alive[0].requires_grad
+
+
+def test_wgrad_does_not_depend_on_the_hint():
+    g = gen(51)
+    cs = [300, 0, 20, 1000]
+    off, cap = segments(cs, 16)
+    a, dy = bf((cap, 264), g).to(DEV), bf((cap, 136), g).to(DEV)
+    got = []
+    for hint in (0, 1, 77, 1 << 20, -5):
+        dw = torch.zeros((4, 136, 264), device=DEV)
+        moe.moe_grouped_gemm_bf16_wgrad(dy, a, i32(off), i32(cs), dw, 1, hint)
+        got.append(dw)
+    assert all(torch.equal(got[0], t) for t in got[1:])

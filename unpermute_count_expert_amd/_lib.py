@@ -598,7 +598,8 @@ def moe_grouped_gemm_bf16_dgrad(dy, w, expert_offsets, counts, dx, rows_hint=0, 
 
 
 def moe_grouped_gemm_bf16_wgrad(dy, a, expert_offsets, counts, dw, accumulate=0, rows_hint=0, stream=None):
-    """dw[e] = (or, with accumulate and fp32 dw, +=) dy[rows of e].T @ a[rows of e]."""
+    """dw[e] = (or, with accumulate and fp32 dw, +=) dy[rows of e].T @ a[rows of e].  rows_hint is taken as by the
+    other products and not read: the tiles go by the matrices' sizes."""
     check_arg(dw, "dw", BF16 + F32, (None, None, None))
     El, n_out, k_in = dw.shape
     check_arg(dy, "dy", BF16, (None, n_out))

@@ -1104,7 +1104,7 @@ int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const int
 
 int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* expert_offsets,
                                 const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n_out,
-                                int32_t k_in, int64_t rows_hint, int32_t dw_dtype, int32_t accumulate, void* dw,
+                                int32_t k_in, int64_t /*rows_hint*/, int32_t dw_dtype, int32_t accumulate, void* dw,
                                 void* stream) {
     int st = check_gemm_bf16(expert_offsets, counts, El, cap_rows, n_out, k_in);
     if (st) return st;
@@ -1123,8 +1123,8 @@ int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int
     st = check_device(&cus);
     if (st) return st;
     HIP_OK(moe::launch_gemm_bf16_wgrad(dy, a, expert_offsets, counts, El, cap_rows, n_out, k_in,
-                                       rows_hint > 0 ? rows_hint : cap_rows, dw_dtype == MOE_DTYPE_F32,
-                                       accumulate != 0, dw, cus, static_cast<hipStream_t>(stream)));
+                                       dw_dtype == MOE_DTYPE_F32, accumulate != 0, dw, cus,
+                                       static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

@@ -922,11 +922,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 //   16 experts, 352 x 200, forward      r 275 17  11  13
 //   4 experts, 376 x 1360, forward      r 41   9  24  31
 //   32 experts, 1792 x 1376, forward    r 106 113 57  71
-// The gradient by the weights has whole matrices as output tiles; 256-row ones
-// where they save more than two fifths of the rounds (290 calls: 1.2% slower
-// than the better on average, always 256 rows 11%; 16 experts of 352 x 200,
-// 4404 rows: 42 us with 128 rows, 59 with 256; 128 of 264 x 360, 16384 rows: 63
-// and 86; 128 of 1536 x 2048, 32768 rows, bf16: 340 and 288).
+// The gradient by the weights has whole matrices as output tiles, whatever the
+// rows (it reads no hint); 256-row ones where they save more than two fifths
+// of the rounds (290 calls: 1.2% slower than the better on average, always 256
+// rows 11%; 16 experts of 352 x 200, 4404 rows: 42 us with 128 rows, 59 with
+// 256; 128 of 264 x 360, 16384 rows: 63 and 86; 128 of 1536 x 2048, 32768
+// rows, bf16: 340 and 288).
 // Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
 template <int MODE, bool F32, bool ACC>
 hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
@@ -980,9 +981,9 @@ hipError_t launch_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const i
 }
 hipError_t launch_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* offsets,
                                   const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
-                                  int64_t rows_hint, bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s) {
+                                  bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s) {
     auto* go = !f32 ? launch<kWgrad, false, false> : accumulate ? launch<kWgrad, true, true> : launch<kWgrad, true, false>;
-    return go(dy, a, offsets, counts, El, cap_rows, n_out, k_in, rows_hint, dw, num_cus, s);
+    return go(dy, a, offsets, counts, El, cap_rows, n_out, k_in, /*rows_hint=*/0, dw, num_cus, s);
 }
 
 }  // namespace moe

@@ -166,7 +166,7 @@ hipError_t launch_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const i
                                   int64_t rows_hint, uint16_t* dx, int num_cus, hipStream_t s);
 hipError_t launch_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* offsets,
                                   const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
-                                  int64_t rows_hint, bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s);
+                                  bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s);
 
 hipError_t launch_silu_mul(const uint16_t* h, int64_t rows, int n, const int32_t* offsets, const int32_t* counts,
                            int El, uint16_t* act, int num_cus, hipStream_t s);
