@@ -405,6 +405,8 @@ int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int
 
 /* SiLU-mul on bf16 rows h [rows,2n] (gate columns [0,n), up [n,2n)):
  *   act[r,c] = bf16( g * u / (1 + exp(-g)) ),  g = h[r,c], u = h[r,n+c].
+ * Computed in fp32: a sigmoid below 2^-126 (g under -87) counts as 0, and in
+ * the gradient a product d * u past the largest float as infinite.
  * act [rows,n].  expert_offsets / counts: NULL = every row valid; otherwise
  * only valid rows are read and written.  act does not overlap h. */
 int moe_silu_mul(const uint16_t* h, int64_t rows, int32_t n, const int32_t* expert_offsets,
