@@ -940,3 +940,36 @@ def test_wgrad_does_not_depend_on_the_hint():
         moe.moe_grouped_gemm_bf16_wgrad(dy, a, i32(off), i32(cs), dw, 1, hint)
         got.append(dw)
     assert all(torch.equal(got[0], t) for t in got[1:])
+
+
+# ---- exact sums over the longest contractions, large permutes, a layer of real width --------
+@pytest.mark.parametrize("n,k", [(65536, 8), (8, 65536), (72, 30000), (30000, 72), (4104, 4168)])
+def test_products_of_small_integers_are_exact(n, k):
+    """Operands in -2 .. 2: every partial sum is an integer below 2^18 + 2^2, exact in fp32 in any order, so the one
+    rounding to bf16 is all that may happen.  A step of the contraction left out, read twice or wrapped wrongly
+    changes most outputs, which the bound on random rounding does not notice at these lengths."""
+    announce("exact products", n, k)
+    g = torch.Generator(device=DEV).manual_seed(n + 3 * k)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device=DEV, dtype=torch.int8).to(BF)
+    cs = [3, 0, 20, 150]
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap).to(DEV)
+    a, dy, w, start = ints(cap, k), ints(cap, n), ints(len(cs), n, k), ints(len(cs), n, k).float()
+    a[~mask], dy[~mask] = float("nan"), float("nan")
+    O, Cn = i32(off), i32(cs)
+    for hint in (1, 64 * len(cs), 150 * len(cs), 1 << 20):
+        out, dx, dw = sentinel((cap, n)), sentinel((cap, k)), start.clone()
+        moe.moe_grouped_gemm_bf16(a, w, O, Cn, out, hint)
+        moe.moe_grouped_gemm_bf16_dgrad(dy, w, O, Cn, dx, hint)
+        moe.moe_grouped_gemm_bf16_wgrad(dy, a, O, Cn, dw, 1)
+        dwb = torch.empty((len(cs), n, k), dtype=BF, device=DEV)
+        moe.moe_grouped_gemm_bf16_wgrad(dy, a, O, Cn, dwb)
+        assert untouched(out, mask.cpu()) and untouched(dx, mask.cpu())
+        for e, c in enumerate(cs):
+            r = slice(off[e], off[e] + c)
+            ae, de, we = a[r].double(), dy[r].double(), w[e].double()
+            dt = de.T.contiguous()
+            assert torch.equal(out[r], (ae @ we.T.contiguous()).to(BF)), (hint, e)
+            assert torch.equal(dx[r], (de @ we).to(BF)), (hint, e)
+            assert torch.equal(dw[e], (dt @ ae + start[e].double()).float()), (hint, e)
+            assert torch.equal(dwb[e], (dt @ ae).to(BF)), (hint, e)
