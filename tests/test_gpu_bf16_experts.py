@@ -973,3 +973,33 @@ def test_products_of_small_integers_are_exact(n, k):
             assert torch.equal(dx[r], (de @ we).to(BF)), (hint, e)
             assert torch.equal(dw[e], (dt @ ae + start[e].double()).float()), (hint, e)
             assert torch.equal(dwb[e], (dt @ ae).to(BF)), (hint, e)
+
+
+@pytest.mark.parametrize("M,topk,K", [(16500, 8, 1152),   # one slice of all columns a pair block, several batches a wave
+                                      (20000, 4, 2048), (250, 8, 8320),   # slices of three groups, the last of one
+                                      (5, 2, 65536), (700, 8, 65536)])
+def test_permute_large_rows(M, topk, K):
+    announce("permute_bf16 large", M, topk, K)
+    Eg, El, align = 128, 100, 32
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x = torch.randint(-2 ** 15, 2 ** 15, (M, K), generator=g, device=DEV, dtype=torch.int32).to(torch.int16)
+    ids = torch.randint(-1, Eg, (M, topk), generator=g, device=DEV, dtype=I32)
+    emap = torch.full((Eg,), -1, dtype=I32, device=DEV)
+    emap[torch.randperm(Eg, generator=g, device=DEV)[:El]] = torch.arange(El, dtype=I32, device=DEV)
+    cap = moe.moe_max_rows(M, topk, El, align)
+    a = torch.full((cap, K), SENT, dtype=torch.int16, device=DEV)
+    counts, off, inv, src = (torch.empty(s, dtype=I32, device=DEV) for s in ((El,), (El + 1,), (M, topk), (cap,)))
+    ws = torch.empty(moe.moe_permute_workspace_size(M, topk, El), dtype=torch.uint8, device=DEV)
+    moe.moe_permute_bf16(x, ids, emap, Eg, El, align, cap, a, counts, off, inv, src, ws)
+    loc = torch.where(ids < 0, -1, emap[ids.clamp(min=0).long()]).reshape(-1).cpu().long()
+    want_c = torch.bincount(loc[loc >= 0], minlength=El)
+    want_o = torch.cat([torch.zeros(1, dtype=torch.int64), ((want_c + align - 1) // align * align).cumsum(0)])
+    order = torch.sort(torch.where(loc < 0, El, loc), stable=True).indices[:int(want_c.sum())]
+    first = want_c.cumsum(0) - want_c
+    rows = want_o[loc[order]] + torch.arange(len(order)) - first[loc[order]]
+    want_inv, want_src = torch.full((M * topk,), -1), torch.full((cap,), -1)
+    want_inv[order], want_src[rows] = rows, order // topk
+    assert torch.equal(counts.cpu().long(), want_c) and torch.equal(off.cpu().long(), want_o)
+    assert torch.equal(inv.reshape(-1).cpu().long(), want_inv) and torch.equal(src.cpu().long(), want_src)
+    valid = (want_src >= 0).to(DEV)
+    assert torch.equal(a[valid], x[want_src.to(DEV)[valid]]) and bool((a[~valid] == SENT).all())
