@@ -1003,3 +1003,34 @@ def test_permute_large_rows(M, topk, K):
     assert torch.equal(inv.reshape(-1).cpu().long(), want_inv) and torch.equal(src.cpu().long(), want_src)
     valid = (want_src >= 0).to(DEV)
     assert torch.equal(a[valid], x[want_src.to(DEV)[valid]]) and bool((a[~valid] == SENT).all())
+
+
+def layer_ref_by_expert(layer, x, ids, tw, dout):
+    """layer_ref, one expert's rows at a time on the GPU."""
+    d = lambda t: t.detach().double().requires_grad_()
+    w13, w2, X, TW = d(layer.w13), d(layer.w2), d(x), d(tw)
+    N, out = layer.N, torch.zeros(x.shape, dtype=F64, device=DEV)
+    local = ids.long() if layer.expert_map is None else layer.expert_map[ids.long()].long()
+    for e in range(layer.El):
+        t, k = (local == e).nonzero(as_tuple=True)
+        h = X[t] @ w13[e].T
+        out = out.index_add(0, t, TW[t, k, None] * ((torch.nn.functional.silu(h[:, :N]) * h[:, N:]) @ w2[e].T))
+    (out * dout.double()).sum().backward()
+    return out.detach().cpu(), X.grad.cpu(), TW.grad.cpu(), w13.grad.cpu(), w2.grad.cpu()
+
+
+@pytest.mark.parametrize("M,Eg,El,topk,K,N", [(1, 32, 32, 8, 2048, 768), (700, 32, 16, 4, 2048, 768),
+                                              (1500, 8, 8, 2, 1152, 640)])
+def test_layer_of_real_width(M, Eg, El, topk, K, N):
+    """As test_layer_forward_backward, on the widths of a layer in use; through autograd."""
+    announce("layer", M, Eg, El, topk, K, N)
+    layer = make_layer(M + 1, Eg, El, K, N)
+    layer.w13.div_(4), layer.w2.div_(2)   # activations of order one
+    x, ids, tw, dout = batch(M + 2, M, K, Eg, topk)
+    ref = layer_ref_by_expert(layer, x, ids, tw, dout)
+    x.requires_grad_(), tw.requires_grad_()
+    out, _ = layer.forward(x, ids, tw)
+    out.backward(dout)
+    for got, want, what in zip((out.detach(), x.grad, tw.grad, layer.grad_w13, layer.grad_w2), ref,
+                               ("out", "dx", "dtw", "dw13", "dw2")):
+        assert rel(got, want) <= 6 * 2.0 ** -8, (what, rel(got, want))
