@@ -19,7 +19,8 @@
 //    dgrad, both in wgrad) lies as in memory, one contraction index a row,
 //    and is transposed on its way to the registers by ds_read_b64_tr_b16.  So
 //    nothing is ever transposed in memory, and both layouts read without
-//    bank conflicts (counted: none).
+//    bank conflicts (counted: 6 to 19 cycles a block and launch, the same for
+//    4096 and 16384 tokens: the tables at its start).
 //  * The buffer descriptor of a granule ends with the last byte that belongs
 //    to it, so ragged rows, the tail of the contraction and whole granules
 //    past the tile arrive as zeros without a read; rows past a segment never
@@ -40,7 +41,7 @@
 //    is down to 1.5-1.8 GHz, and a step's fragment reads and loads take the
 //    LDS as many cycles (98 KB out and 32 KB in a phase, 128 bytes a cycle)
 //    as the phase's MFMAs take the matrix units.  dgrad runs at 1070, wgrad
-//    at 920 (fp32 gradients) and 1060 TFLOP/s (bf16).
+//    at 910 (fp32 gradients; accumulating 770) and 1060 TFLOP/s (bf16).
 //  * Not kept: four waves of 128 x 128 with fragments double-buffered (one
 //    wave per SIMD; 0.96 ms), steps of 32 in four stages (0.96 ms, half-line
 //    reads), a prefetch of later steps into L2 (slower by its own reads: the
@@ -381,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         c.valid = c.t < t_hi;
         if (!c.valid) return;
         if constexpr (MODE == kWgrad) {
-            c.e = (int)((uint32_t)c.t / (uint32_t)(ntm_w * ntn));   // at most 1024 * 256 * 256 tiles
+            c.e = (int)((uint32_t)c.t / (uint32_t)(ntm_w * ntn));   // at most 1024 * 512 * 256 tiles
         } else {
             while (c.e + 1 < El && (int64_t)s_at[c.e + 1] * ntn <= c.t) ++c.e;
             c.e = __builtin_amdgcn_readfirstlane(c.e);
@@ -909,9 +910,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 // microseconds, for rows_hint rows spread evenly and a part of a tile more an
 // expert for raggedness; the constants are fitted to 538 measured calls (1 to
 // 131072 rows, 4 to 128 experts, widths of 128 to 4096, even and skewed
-// routing), in which the choice is 1.2% slower than the best of the three on
-// average (by rows per expert alone 9%).  Measured (k_few, 128 rows, 256 rows;
-// r rows per expert):
+// routing; those under 8 us were fitted as 8), in which the choice is 1.2%
+// slower than the best of the three on average (by rows per expert alone 9%),
+// over 20% slower in 15 and 52% at worst (four experts of 2048 x 1024 or 60 to
+// 128 narrow ones, where a part of a round decides; 30 experts of 1232 x 1056
+// under skew 36%, as the rows are taken to lie evenly).  Measured (k_few, 128
+// rows, 256 rows; r rows per expert):
 //   128 experts, 1536 x 2048, forward   r 4  138 139 142   r 16 158 143 144
 //                                       r 96 480 160 162   r 128 616 211 177
 //                             dgrad     r 4  149 142 141   r 16 171 145 140
@@ -924,8 +928,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 //   32 experts, 1792 x 1376, forward    r 106 113 57  71
 // The gradient by the weights has whole matrices as output tiles, whatever the
 // rows (it reads no hint); 256-row ones where they save more than two fifths
-// of the rounds (290 calls: 1.2% slower than the better on average, always 256
-// rows 11%; 16 experts of 352 x 200, 4404 rows: 42 us with 128 rows, 59 with
+// of the rounds (290 calls: 1.2% slower than the better on average, 24% at
+// worst, always 256 rows 11%; 16 experts of 352 x 200, 4404 rows: 42 us with 128 rows, 59 with
 // 256; 128 of 264 x 360, 16384 rows: 63 and 86; 128 of 1536 x 2048, 32768
 // rows, bf16: 340 and 288).
 // Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
