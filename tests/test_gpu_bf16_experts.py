@@ -1034,3 +1034,144 @@ def test_layer_of_real_width(M, Eg, El, topk, K, N):
     for got, want, what in zip((out.detach(), x.grad, tw.grad, layer.grad_w13, layer.grad_w2), ref,
                                ("out", "dx", "dtw", "dw13", "dw2")):
         assert rel(got, want) <= 6 * 2.0 ** -8, (what, rel(got, want))
+
+
+# ---- offsets past 32 bits, tensors that start inside a line, nothing at all -------------------
+def at_16_bytes(t):
+    """A copy that starts 16 bytes past a 256-byte boundary."""
+    buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[8 if t.dtype == BF else 4:]
+    return buf[:t.numel()].view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("hint", [1, 1 << 20])
+def test_products_past_32_bits(hint):
+    """Rows, weights and gradients whose offsets pass 2^31 elements and 2^32 bytes: segments at a buffer's two ends."""
+    announce("products past 32 bits", hint)
+    E, n, k, cap = 140, 4096, 4096, 600_000
+    cs = [0] * E
+    cs[0], cs[70], cs[E - 1] = 5, 3, 260
+    off = [0] + [16] * 69 + [cap - 400] + [cap - 384] * 69 + [cap]
+    assert len(off) == E + 1 and (cap - 384) * k > 2 ** 31 and (E - 1) * n * k > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(hint)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device=DEV, dtype=torch.int8).to(BF)
+    rows = {e: slice(off[e], off[e] + cs[e]) for e in (0, 70, E - 1)}
+    a, dy, out, dx = (torch.empty((cap, 4096), dtype=BF, device=DEV) for _ in range(4))
+    w, dw = torch.empty((E, n, k), dtype=BF, device=DEV), torch.empty((E, n, k), device=DEV)
+    for e, r in rows.items():
+        a[r], dy[r], w[e] = ints(cs[e], k), ints(cs[e], n), ints(n, k)
+    out[cap - 124:], dx[cap - 124:] = 77, 77
+    O, Cn = i32(off), i32(cs)
+    moe.moe_grouped_gemm_bf16(a, w, O, Cn, out, hint)
+    moe.moe_grouped_gemm_bf16_dgrad(dy, w, O, Cn, dx, hint)
+    moe.moe_grouped_gemm_bf16_wgrad(dy, a, O, Cn, dw)
+    for e, r in rows.items():
+        ae, de, we = a[r].double(), dy[r].double(), w[e].double()
+        assert torch.equal(out[r], (ae @ we.T.contiguous()).to(BF)) and torch.equal(dx[r], (de @ we).to(BF))
+        assert torch.equal(dw[e], (de.T.contiguous() @ ae).float())
+    assert not dw[1].any() and not dw[E - 2].any()
+    assert (out[cap - 124:] == 77).all() and (dx[cap - 124:] == 77).all()
+
+
+def test_row_operators_past_32_bits():
+    announce("row operators past 32 bits")
+    # SiLU-mul: the valid rows at the end of a buffer of 4.9 G elements
+    rows, n = 600_000, 4096
+    h, d, act = (torch.empty((rows, w), dtype=BF, device=DEV) for w in (2 * n, n, n))
+    g = torch.Generator(device=DEV).manual_seed(1)
+    h[-50:], d[-50:] = torch.randn((50, 2 * n), generator=g, device=DEV), torch.randn((50, n), generator=g, device=DEV)
+    small = [t[-50:].clone() for t in (h, d)]
+    O, Cn = i32([rows - 50, rows]), i32([50])
+    moe.moe_silu_mul(h, n, act, O, Cn, 1)
+    moe.moe_silu_mul_bwd(h, d, n, h, O, Cn, 1)
+    want_act, want_dh = torch.empty_like(small[1]), torch.empty_like(small[0])
+    moe.moe_silu_mul(small[0], n, want_act)
+    moe.moe_silu_mul_bwd(*small, n, want_dh)
+    assert torch.equal(act[-50:], want_act) and torch.equal(h[-50:], want_dh)
+    del h, d, act
+    # the weighted unpermute's gradient: rows at both ends
+    y, dy = torch.empty((rows, 4096), dtype=BF, device=DEV), torch.empty((rows, 4096), dtype=BF, device=DEV)
+    inv = i32([[0, rows - 1], [rows - 2, -1]])
+    named = [0, rows - 1, rows - 2]
+    y[named] = torch.randint(-2, 3, (3, 4096), generator=g, device=DEV, dtype=torch.int32).to(BF)
+    dout = torch.randint(-2, 3, (2, 4096), generator=g, device=DEV, dtype=torch.int32).to(BF)
+    tw, dtw = torch.tensor([[2.0, 3.0], [-1.0, 5.0]], device=DEV), torch.empty((2, 2), device=DEV)
+    moe.moe_unpermute_weight_reduce_bwd(dout, y, inv, tw, dy, dtw)
+    assert torch.equal(dy[named].float(), torch.stack([dout[0] * 2.0, dout[0] * 3.0, -dout[1]]).float())
+    want = torch.stack([(y[r].double() * dout[t].double()).sum() for r, t in ((0, 0), (rows - 1, 0), (rows - 2, 1))])
+    assert torch.equal(dtw.reshape(-1)[:3].double(), want) and dtw[1, 1] == 0
+    del y, dy
+    # the permute: 800000 rows of 4096 out of 100000 tokens, checked through its own indices
+    M, topk, K, El = 100_000, 8, 4096, 16
+    x = torch.randint(-2 ** 15, 2 ** 15, (M, K), generator=g, device=DEV, dtype=torch.int32).to(torch.int16)
+    ids = torch.randint(0, El, (M, topk), generator=g, device=DEV, dtype=I32)
+    cap = moe.moe_max_rows(M, topk, El, 16)
+    a = torch.empty((cap, K), dtype=torch.int16, device=DEV)
+    counts, off, inv, src = (torch.empty(s, dtype=I32, device=DEV) for s in ((El,), (El + 1,), (M, topk), (cap,)))
+    ws = torch.empty(moe.moe_permute_workspace_size(M, topk, El), dtype=torch.uint8, device=DEV)
+    moe.moe_permute_bf16(x, ids, None, El, El, 16, cap, a, counts, off, inv, src, ws)
+    assert torch.equal(counts.long(), torch.bincount(ids.reshape(-1).long(), minlength=El))
+    assert int(inv.max()) * K > 2 ** 31 and inv.unique().numel() == M * topk
+    for k in range(topk):
+        for lo in range(0, M, 20_000):
+            assert torch.equal(a[inv[lo:lo + 20_000, k].long()], x[lo:lo + 20_000])
+
+
+def test_clip_past_32_bits():
+    """One gradient of 2^32 and some elements."""
+    announce("clip past 32 bits")
+    m = 2 ** 32 + 13
+    t = torch.ones(m, dtype=BF, device=DEV)
+    t[-1] = 2.0
+    s, nrm = clip([t], None, 2.0 ** 8)
+    assert s == m + 3 and abs(nrm - (m + 3) ** 0.5) <= 2.0 ** -24 * nrm
+    # the factor, 2^8 / sqrt(2^32 + 16), is 2^-8 but for less than 2^-28 of it
+    assert t[-1] == 2.0 ** -7 and t[0] == 2.0 ** -8
+    assert int((t[:-1] == 2.0 ** -8).sum()) == m - 1
+
+
+@pytest.mark.parametrize("hint", [1, 1 << 20])
+def test_tensors_that_start_inside_a_line(hint):
+    """The least alignment that the entry points take, 16 bytes, gives the bits of aligned tensors."""
+    g = gen(61)
+    cs, n, k = [70, 0, 3, 300], 264, 136
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    a, dy, w, h = (bf(s, g).to(DEV) for s in ((cap, k), (cap, n), (4, n, k), (cap, 2 * n)))
+    tw, inv = torch.rand((cap, 1), generator=g).to(DEV), torch.randperm(cap, generator=g).to(I32)[:, None].to(DEV)
+    x, dout = bf((cap, 256), g).to(DEV), bf((cap, 256), g).to(DEV)
+
+    def run(c):
+        O, Cn = c(i32(off)), c(i32(cs))
+        out, dx, act, dh = (c(sentinel(s)) for s in ((cap, n), (cap, k), (cap, n), (cap, 2 * n)))
+        dwf, dwb = c(torch.ones((4, n, k), device=DEV)), c(torch.ones((4, n, k), dtype=BF, device=DEV))
+        moe.moe_grouped_gemm_bf16(c(a), c(w), O, Cn, out, hint)
+        moe.moe_grouped_gemm_bf16_dgrad(c(dy), c(w), O, Cn, dx, hint)
+        moe.moe_grouped_gemm_bf16_wgrad(c(dy), c(a), O, Cn, dwf, 1)
+        moe.moe_grouped_gemm_bf16_wgrad(c(dy), c(a), O, Cn, dwb)
+        moe.moe_silu_mul(c(h), n, act, O, Cn, 4)
+        moe.moe_silu_mul_bwd(c(h), c(dy), n, dh, O, Cn, 4)
+        du, dtw = c(sentinel((cap, 256))), c(torch.ones((cap, 1), device=DEV))
+        moe.moe_unpermute_weight_reduce_bwd(c(dout), c(x), c(inv), c(tw), du, dtw)
+        return out, dx, act, dh, dwf, dwb, du, dtw
+
+    for p, q in zip(run(at_16_bytes), run(lambda t: t)):
+        assert p.data_ptr() % 256 == 16 and torch.equal(p.view(torch.int16), q.view(torch.int16))
+    assert mask.any()
+
+
+def test_products_of_nothing():
+    """No rows at all: an overwritten gradient is zeros, an accumulated one stays."""
+    O, Cn = i32([0, 0, 0]), i32([0, 0])
+    empty = torch.empty((0, 72), dtype=BF, device=DEV)
+    a = torch.empty((0, 520), dtype=BF, device=DEV)
+    for dt in (F32, BF):
+        dw = torch.full((2, 72, 520), 3.0, dtype=dt, device=DEV)
+        moe.moe_grouped_gemm_bf16_wgrad(empty, a, O, Cn, dw)
+        assert not dw.any()
+    dw = torch.full((2, 72, 520), 3.0, device=DEV)
+    moe.moe_grouped_gemm_bf16_wgrad(empty, a, O, Cn, dw, 1)
+    assert (dw == 3.0).all()
+    w = torch.empty((2, 72, 520), dtype=BF, device=DEV)
+    moe.moe_grouped_gemm_bf16(a, w, O, Cn, empty)
+    moe.moe_grouped_gemm_bf16_dgrad(empty, w, O, Cn, a)
+    moe.moe_silu_mul(torch.empty((0, 144), dtype=BF, device=DEV), 72, empty, O, Cn, 2)
