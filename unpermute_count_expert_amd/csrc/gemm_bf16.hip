@@ -612,7 +612,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     // (starting the sums at it would round at it every 32 rows).  It is read
     // in the stores' own pieces, kOld row blocks ahead of its use: the step's
     // fragments are dead here and leave the registers.  Bound by its bytes, 8 an
-    // element (4096 tokens, 1536 x 2048: 606 us, 5.6 TB/s; one, two and four
+    // element (4096 tokens, 1536 x 2048: 606 us, 5.7 TB/s; one, two and four
     // blocks ahead: 627, 620, 606), non-temporal as the stores are (read
     // plainly 678; 725 tokens, 704 x 1256, whose rows are not whole lines: 204,
     // non-temporal 233).
@@ -929,9 +929,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 // The gradient by the weights has whole matrices as output tiles, whatever the
 // rows (it reads no hint); 256-row ones where they save more than two fifths
 // of the rounds (290 calls: 1.2% slower than the better on average, 24% at
-// worst, always 256 rows 11%; 16 experts of 352 x 200, 4404 rows: 42 us with 128 rows, 59 with
-// 256; 128 of 264 x 360, 16384 rows: 63 and 86; 128 of 1536 x 2048, 32768
-// rows, bf16: 340 and 288).
+// worst, always 256 rows 11%; 16 experts of 352 x 200, 4404 rows: 42 us with
+// 128 rows, 59 with 256; 128 of 264 x 360, 16384 rows: 63 and 86; 128 of
+// 1536 x 2048, 32768 rows, bf16: 340 and 288).
 // Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
 template <int MODE, bool F32, bool ACC>
 hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
