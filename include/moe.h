@@ -434,6 +434,85 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
                                     const int32_t* inv_perm, const float* topk_weights, int64_t Mc, int32_t K,
                                     int32_t topk, uint16_t* dy, float* dweights, void* stream);
 
+/* ---- gated experts in one kernel, and 8-bit checkpoints -----------------------
+ * The gate and up products with SiLU-mul in one kernel, the down product's
+ * gradient by the rows with SiLU-mul's backward in one kernel, and what a
+ * training step keeps between them: gate and up rows in bf16 or in 8 bits,
+ * tokens in 8 bits.  Rows, segments, widths and rows_hint as above.
+ *
+ * 8 bits: every 32 values along a row (widths are multiples of 32) are 32 e4m3
+ * codes and one scale byte b (E8M0) and stand for code * 2^(b - 127).  The
+ * scale is the least power of two that brings the block's largest magnitude to
+ * 448 or below, but at least 2^-117; codes are rounded to nearest even, so a
+ * value is off by at most 2^-4 of itself, or 2^-10 of the scale if that is
+ * more.  A block that holds an infinity or a NaN has b = 255 and is NaN
+ * throughout.  What is restored is exact in bf16.  b = 0, never written, reads
+ * as 0. */
+
+/* x [rows,width] bf16 -> codes q [rows,width], scales [rows,width/32].
+ * width: positive multiple of 32 up to 65536. */
+int moe_checkpoint(const uint16_t* x, int64_t rows, int32_t width, uint8_t* q, uint8_t* scales, void* stream);
+
+/* Restores rows: out[row] = bf16 of row t, row = inv_perm[t,k], for every t and
+ * k with 0 <= row < out_rows (rows that no pair names are not written; in a
+ * row named by two pairs each element is either's).  inv_perm NULL: out[t] =
+ * row t for t < out_rows.  q [Mc,width], scales [Mc,width/32], inv_perm
+ * [Mc,topk], out [out_rows,width] bf16; out overlaps no input. */
+int moe_checkpoint_restore(const uint8_t* q, const uint8_t* scales, int64_t Mc, int32_t width,
+                           const int32_t* inv_perm, int32_t topk, uint16_t* out, int64_t out_rows, void* stream);
+
+/* An earlier permute's rows for another tensor: out[inv_perm[t,k]] = x[t], as
+ * moe_checkpoint_restore for bf16 rows, and row_weights[inv_perm[t,k]] =
+ * topk_weights[t,k] where given (both or neither).  x [Mc,K], out [out_rows,K]
+ * bf16, K a positive multiple of 8 up to 65536; topk_weights [Mc,topk],
+ * row_weights [out_rows] fp32. */
+int moe_permute_rows(const uint16_t* x, const int32_t* inv_perm, const float* topk_weights, int64_t Mc, int32_t K,
+                     int32_t topk, uint16_t* out, int64_t out_rows, float* row_weights, void* stream);
+
+/* For every valid row r of expert e, with h[r,j] = sum_k a[r,k] * w13[e,j,k]
+ * (gate columns j < n, up columns n <= j < 2n) in fp32:
+ *   act[r,c] = bf16( g * u / (1 + exp(-g)) ),  g = h[r,c], u = h[r,n+c],
+ * from the sums themselves, and what the backward pass needs of h:
+ *   h NULL: nothing;  h given, h_scales NULL: bf16 [cap_rows,2n];
+ *   both given: 8 bits, codes [cap_rows,2n] and scales [cap_rows,2n/32], n a
+ *   multiple of 32.
+ * a [cap_rows,k_in], w13 [El,2n,k_in], act [cap_rows,n]; n a positive multiple
+ * of 8 up to 32768.  No output overlaps an input or another output.  The
+ * sigmoid as in moe_silu_mul. */
+int moe_grouped_gemm_bf16_silu_mul(const uint16_t* a, const uint16_t* w13, const int32_t* expert_offsets,
+                                   const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n, int32_t k_in,
+                                   int64_t rows_hint, uint16_t* act, void* h, uint8_t* h_scales, void* stream);
+
+/* The down product's gradient by the rows, through SiLU-mul: for every valid
+ * row r of expert e and c < n, with d = sum_k dy[r,k] * w2[e,k,c] in fp32, g
+ * and u from h (bf16, or 8 bits with h_scales), s = 1 / (1 + exp(-g)) and p =
+ * row_weights[r] (1 if NULL),
+ *   dh[r,c] = bf16( p * d * u * s * (1 + g * (1 - s)) ),
+ *   dh[r,n+c] = bf16( p * d * g * s ),
+ *   act[r,c] = bf16( p * g * s * u )                     (act not NULL),
+ *   dots[r,i] = sum of g * s * u * d over the columns c of [64 i, 64 i + 64)
+ *                                                        (dots not NULL).
+ * With dy the rows of the layer's output gradient (moe_permute_rows) and p the
+ * router's weights, act is what the gradient by w2 needs beside dy, and
+ * moe_topk_weights_bwd makes the router weights' gradient of dots: the down
+ * product's output is not needed.  With dy already weighted, p is 1 and the
+ * dots are not the weights' gradient.  dy [cap_rows,k_out], w2 [El,k_out,n],
+ * h and dh [cap_rows,2n], act [cap_rows,n], row_weights [cap_rows], dots
+ * [cap_rows, (n + 63) / 64]; n as above.  dh may be h itself where that is
+ * bf16 (in place); apart from that no output overlaps an input or another
+ * output. */
+int moe_grouped_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w2, const int32_t* expert_offsets,
+                                         const int32_t* counts, int32_t El, int64_t cap_rows, int32_t k_out,
+                                         int32_t n, int64_t rows_hint, const void* h, const uint8_t* h_scales,
+                                         const float* row_weights, uint16_t* dh, uint16_t* act, float* dots,
+                                         void* stream);
+
+/* dweights[t,k] = sum_i dots[inv_perm[t,k], i] where 0 <= inv_perm[t,k] < rows,
+ * else 0, in a fixed order.  dots [rows,num_dots] fp32, 1 <= num_dots <= 1024,
+ * inv_perm and dweights [Mc,topk]. */
+int moe_topk_weights_bwd(const float* dots, int32_t num_dots, int64_t rows, const int32_t* inv_perm, int64_t Mc,
+                         int32_t topk, float* dweights, void* stream);
+
 /* Global gradient norm over many tensors, and clipping.  A tensor of the
  * list: `grad` its values (contiguous, aligned to its element only), `out`
  * where moe_grad_clip writes (grad itself, or memory that no other field of

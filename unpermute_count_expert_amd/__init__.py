@@ -14,5 +14,6 @@ from ._lib import (MOE_ACT_IDENTITY, MOE_ACT_SILU_MUL, MoeError, MoeProblem, loa
                    moe_forward_plan_info, moe_unpermute_weight_reduce, problem, MOE_DTYPE_BF16, MOE_DTYPE_F32,
                    moe_permute_bf16, moe_grouped_gemm_bf16, moe_grouped_gemm_bf16_dgrad, moe_grouped_gemm_bf16_wgrad,
                    moe_silu_mul, moe_silu_mul_bwd, moe_unpermute_weight_reduce_bwd, moe_grad_workspace_size,
-                   moe_grad_sumsq, moe_grad_clip)
+                   moe_grad_sumsq, moe_grad_clip, moe_checkpoint, moe_checkpoint_restore, moe_permute_rows,
+                   moe_grouped_gemm_bf16_silu_mul, moe_grouped_gemm_bf16_dgrad_silu_mul, moe_topk_weights_bwd)
 from .layer import MoeLayer, MoeTrainLayer  # noqa: F401

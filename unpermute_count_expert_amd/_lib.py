@@ -52,7 +52,9 @@ EXPORTS = ["moe_status_string", "moe_last_error", "moe_max_rows", "moe_grouped_g
            "moe_grouped_gemm_fp8_small", "moe_act_quant_partials", "moe_unpermute_partials",
            "moe_forward_plan_info", "moe_permute_bf16", "moe_grouped_gemm_bf16", "moe_grouped_gemm_bf16_dgrad",
            "moe_grouped_gemm_bf16_wgrad", "moe_silu_mul", "moe_silu_mul_bwd", "moe_unpermute_weight_reduce_bwd",
-           "moe_grad_workspace_size", "moe_grad_sumsq", "moe_grad_clip"]
+           "moe_grad_workspace_size", "moe_grad_sumsq", "moe_grad_clip", "moe_checkpoint", "moe_checkpoint_restore",
+           "moe_permute_rows", "moe_grouped_gemm_bf16_silu_mul", "moe_grouped_gemm_bf16_dgrad_silu_mul",
+           "moe_topk_weights_bwd"]
 
 _lib = None
 
@@ -105,6 +107,12 @@ def load() -> C.CDLL:
         L.moe_grad_workspace_size.argtypes = [I32, C.POINTER(SZ)]
         L.moe_grad_sumsq.argtypes = [P, I32, P, P, SZ, P]
         L.moe_grad_clip.argtypes = [P, I32, P, C.c_float, P, P]
+        L.moe_checkpoint.argtypes = [P, I64, I32, P, P, P]
+        L.moe_checkpoint_restore.argtypes = [P, P, I64, I32, P, I32, P, I64, P]
+        L.moe_permute_rows.argtypes = [P, P, P, I64, I32, I32, P, I64, P, P]
+        L.moe_grouped_gemm_bf16_silu_mul.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, P, P, P, P]
+        L.moe_grouped_gemm_bf16_dgrad_silu_mul.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, P, P, P, P, P, P, P]
+        L.moe_topk_weights_bwd.argtypes = [P, I32, I64, P, I64, I32, P, P]
         L.moe_noalloc_scratch_bytes.argtypes = []; L.moe_noalloc_scratch_bytes.restype = SZ
         for name in EXPORTS:
             if name not in ("moe_status_string", "moe_last_error", "moe_max_rows", "moe_grouped_gemm_tile_rows",
@@ -147,6 +155,7 @@ BF16 = (torch.int16, torch.bfloat16)          # bf16 values or their raw bits
 E4M3 = (torch.uint8, torch.float8_e4m3fn)     # e4m3 codes
 I32 = (torch.int32,)
 F32 = (torch.float32,)
+E8M0 = (torch.uint8, torch.float8_e8m0fnu)    # power-of-two scales
 
 
 def check_arg(t, name: str, dtypes, shape=None, min_rows=None, optional=False):
@@ -654,6 +663,112 @@ def moe_unpermute_weight_reduce_bwd(dout, y, inv_perm, topk_weights, dy, dweight
     _check(load().moe_unpermute_weight_reduce_bwd(_ptr(dout), _ptr(y), y_rows, _ptr(inv_perm), _ptr(topk_weights),
                                                   Mc, K, topk, _ptr(dy), _ptr(dweights), _stream(stream)),
            "moe_unpermute_weight_reduce_bwd")
+
+
+# ---- gated experts in one kernel, and 8-bit checkpoints -----------------------------
+CHECKPOINT_BLOCK = 32   # values that share a scale
+
+
+def moe_checkpoint(x, q, q_s, stream=None):
+    """bf16 rows x [rows, width] as e4m3 codes q [rows, width] with a power-of-two scale for every 32 values, q_s
+    [rows, width / 32]."""
+    check_arg(x, "x", BF16, (None, None))
+    rows, width = x.shape
+    check_arg(q, "q", E4M3, (rows, width))
+    check_arg(q_s, "q_s", E8M0, (rows, width // CHECKPOINT_BLOCK))
+    check_device(x, q, q_s)
+    _check(load().moe_checkpoint(_ptr(x), rows, width, _ptr(q), _ptr(q_s), _stream(stream)), "moe_checkpoint")
+
+
+def moe_checkpoint_restore(q, q_s, out, inv_perm=None, stream=None):
+    """out[inv_perm[t, k]] = bf16 of checkpoint row t for every pair with a row of out; without inv_perm out = the
+    rows in their order."""
+    check_arg(q, "q", E4M3, (None, None))
+    Mc, width = q.shape
+    check_arg(q_s, "q_s", E8M0, (Mc, width // CHECKPOINT_BLOCK))
+    check_arg(inv_perm, "inv_perm", I32, (Mc, None), optional=True)
+    topk = 1 if inv_perm is None else inv_perm.shape[1]
+    check_arg(out, "out", BF16, (Mc if inv_perm is None else None, width))
+    check_device(q, q_s, inv_perm, out)
+    _check(load().moe_checkpoint_restore(_ptr(q), _ptr(q_s), Mc, width, _ptr(inv_perm), topk, _ptr(out), out.shape[0],
+                                         _stream(stream)), "moe_checkpoint_restore")
+
+
+def moe_permute_rows(x, inv_perm, out, topk_weights=None, row_weights=None, stream=None):
+    """out[inv_perm[t, k]] = x[t] and row_weights[inv_perm[t, k]] = topk_weights[t, k] for every pair with a row of
+    out: an earlier permute for another tensor."""
+    check_arg(x, "x", BF16, (None, None))
+    Mc, K = x.shape
+    check_arg(inv_perm, "inv_perm", I32, (Mc, None))
+    topk = inv_perm.shape[1]
+    check_arg(out, "out", BF16, (None, K))
+    check_arg(topk_weights, "topk_weights", F32, (Mc, topk), optional=True)
+    check_arg(row_weights, "row_weights", F32, (out.shape[0],), optional=True)
+    check_device(x, inv_perm, out, topk_weights, row_weights)
+    _check(load().moe_permute_rows(_ptr(x), _ptr(inv_perm), _ptr(topk_weights), Mc, K, topk, _ptr(out), out.shape[0],
+                                   _ptr(row_weights), _stream(stream)), "moe_permute_rows")
+
+
+def _check_kept(h, h_s, cap_rows, n, optional=False):
+    """Gate and up rows: bf16, or with h_s e4m3 codes."""
+    if h_s is None:
+        check_arg(h, "h", BF16, (cap_rows, 2 * n), None, optional)
+    else:
+        check_arg(h, "h", E4M3, (cap_rows, 2 * n))
+        check_arg(h_s, "h_s", E8M0, (cap_rows, 2 * n // CHECKPOINT_BLOCK))
+
+
+def moe_grouped_gemm_bf16_silu_mul(a, w13, expert_offsets, counts, act, h=None, h_s=None, rows_hint=0, stream=None):
+    """act[r] = silu(a[r] @ gate[e].T) * (a[r] @ up[e].T) over the valid rows r of every expert e, w13 [El, 2n, k]
+    the gate's and up's rows.  h [cap_rows, 2n] receives the two products for the backward pass: bf16, or with h_s
+    [cap_rows, 2n / 32] in 8 bits as by moe_checkpoint; None: not kept."""
+    check_arg(a, "a", BF16, (None, None))
+    cap_rows, k = a.shape
+    check_arg(w13, "w13", BF16, (None, None, k))
+    El, two_n, _ = w13.shape
+    if two_n % 2:
+        raise ValueError(f"w13 has {two_n} rows an expert; expected as many for up as for gate")
+    n = two_n // 2
+    _check_segments(expert_offsets, counts, El)
+    check_arg(act, "act", BF16, (cap_rows, n))
+    _check_kept(h, h_s, cap_rows, n, True)
+    check_device(a, w13, expert_offsets, counts, act, h, h_s)
+    _check(load().moe_grouped_gemm_bf16_silu_mul(_ptr(a), _ptr(w13), _ptr(expert_offsets), _ptr(counts), El, cap_rows,
+                                                 n, k, rows_hint, _ptr(act), _ptr(h), _ptr(h_s), _stream(stream)),
+           "moe_grouped_gemm_bf16_silu_mul")
+
+
+def moe_grouped_gemm_bf16_dgrad_silu_mul(dy, w2, expert_offsets, counts, h, dh, act=None, h_s=None, row_weights=None,
+                                         dots=None, rows_hint=0, stream=None):
+    """dh = SiLU-mul's gradient at h (bf16, or with h_s 8 bits) of d = dy[r] @ w2[e], times row_weights[r], over the
+    valid rows.  act, if given, receives row_weights * silu(gate) * up, dots [cap_rows, ceil(n / 64)] silu(gate) * up
+    * d summed over every 64 columns.  dh may be a bf16 h."""
+    check_arg(w2, "w2", BF16, (None, None, None))
+    El, k, n = w2.shape
+    check_arg(dy, "dy", BF16, (None, k))
+    cap_rows = dy.shape[0]
+    _check_segments(expert_offsets, counts, El)
+    _check_kept(h, h_s, cap_rows, n)
+    check_arg(dh, "dh", BF16, (cap_rows, 2 * n))
+    check_arg(act, "act", BF16, (cap_rows, n), None, True)
+    check_arg(row_weights, "row_weights", F32, (cap_rows,), None, True)
+    check_arg(dots, "dots", F32, (cap_rows, (n + 63) // 64), None, True)
+    check_device(dy, w2, expert_offsets, counts, h, dh, act, h_s, row_weights, dots)
+    _check(load().moe_grouped_gemm_bf16_dgrad_silu_mul(_ptr(dy), _ptr(w2), _ptr(expert_offsets), _ptr(counts), El,
+                                                       cap_rows, k, n, rows_hint, _ptr(h), _ptr(h_s),
+                                                       _ptr(row_weights), _ptr(dh), _ptr(act), _ptr(dots),
+                                                       _stream(stream)), "moe_grouped_gemm_bf16_dgrad_silu_mul")
+
+
+def moe_topk_weights_bwd(dots, inv_perm, dweights, stream=None):
+    """dweights[t, k] = dots[inv_perm[t, k]].sum(), 0 for pairs without a row."""
+    check_arg(dots, "dots", F32, (None, None))
+    check_arg(inv_perm, "inv_perm", I32, (None, None))
+    Mc, topk = inv_perm.shape
+    check_arg(dweights, "dweights", F32, (Mc, topk))
+    check_device(dots, inv_perm, dweights)
+    _check(load().moe_topk_weights_bwd(_ptr(dots), dots.shape[1], dots.shape[0], _ptr(inv_perm), Mc, topk,
+                                       _ptr(dweights), _stream(stream)), "moe_topk_weights_bwd")
 
 
 _dtype_of = operator.attrgetter("dtype")

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "moe.h"
@@ -996,6 +997,48 @@ int check_silu(int64_t rows, int32_t n, const int32_t* expert_offsets, const int
     return MOE_OK;
 }
 
+// No output overlaps an input or another output; a null argument is not given.
+struct Span {
+    const void* p;
+    size_t bytes;
+    const char* name;
+};
+int check_outputs(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            REQUIRE(!o->p || !i.p || !overlaps(o->p, o->bytes, i.p, i.bytes), MOE_ERR_INVALID_ARG, "%s overlaps %s",
+                    o->name, i.name);
+        for (const Span* i = outs.begin(); i != o; ++i)
+            REQUIRE(!o->p || !i->p || !overlaps(o->p, o->bytes, i->p, i->bytes), MOE_ERR_INVALID_ARG,
+                    "%s overlaps %s", o->name, i->name);
+    }
+    return MOE_OK;
+}
+
+int check_checkpoint(int64_t rows, int32_t width) {
+    REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "rows=%lld", (long long)rows);
+    REQUIRE(width > 0 && width % 32 == 0 && width <= 65536, MOE_ERR_SHAPE,
+            "width=%d is not a positive multiple of 32 up to 65536", width);
+    return MOE_OK;
+}
+
+int check_pairs(int64_t Mc, int32_t topk, int64_t rows) {
+    REQUIRE(Mc >= 0 && rows >= 0 && rows < (int64_t(1) << 31), MOE_ERR_SHAPE, "Mc=%lld rows=%lld", (long long)Mc,
+            (long long)rows);
+    REQUIRE(topk >= 1 && topk <= 256, MOE_ERR_SHAPE, "topk=%d outside [1,256]", topk);
+    REQUIRE(Mc < (int64_t(1) << 31) / topk, MOE_ERR_SHAPE, "too many tokens");
+    return MOE_OK;
+}
+
+// The gated products: n columns of gate and of up, k of the rows.
+int check_gated(const int32_t* expert_offsets, const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n,
+                int32_t k, const void* h, const uint8_t* h_scales) {
+    REQUIRE(n > 0 && n % 8 == 0 && n <= 32768, MOE_ERR_SHAPE, "n=%d is not a positive multiple of 8 up to 32768", n);
+    REQUIRE(h_scales == nullptr || n % 32 == 0, MOE_ERR_SHAPE, "n=%d is not a multiple of 32: h has no 8-bit form", n);
+    REQUIRE(h_scales == nullptr || h != nullptr, MOE_ERR_INVALID_ARG, "h_scales without h");
+    return check_gemm_bf16(expert_offsets, counts, El, cap_rows, n, k);
+}
+
 int check_grads(const moe_grad_tensor* t, int32_t num, bool clip) {
     REQUIRE(num >= 0 && num <= (1 << 20), MOE_ERR_SHAPE, "num_tensors=%d outside [0, 2^20]", num);
     REQUIRE(num == 0 || t != nullptr, MOE_ERR_INVALID_ARG, "tensors is NULL");
@@ -1195,6 +1238,156 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
     if (st) return st;
     HIP_OK(moe::launch_unpermute_bwd(dout, y, y_rows, inv_perm, topk_weights, Mc, K, topk, dy, dweights, cus,
                                      static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_checkpoint(const uint16_t* x, int64_t rows, int32_t width, uint8_t* q, uint8_t* scales, void* stream) {
+    int st = check_checkpoint(rows, width);
+    if (st) return st;
+    if (rows == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(scales);
+    const size_t values = (size_t)rows * width;
+    st = check_outputs({{q, values, "q"}, {scales, values / 32, "scales"}}, {{x, values * 2, "x"}});
+    if (st) return st;
+    st = check_device(nullptr);
+    if (st) return st;
+    HIP_OK(moe::launch_checkpoint(x, (int64_t)values, q, scales, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_checkpoint_restore(const uint8_t* q, const uint8_t* scales, int64_t Mc, int32_t width,
+                           const int32_t* inv_perm, int32_t topk, uint16_t* out, int64_t out_rows, void* stream) {
+    int st = check_checkpoint(Mc, width);
+    if (st) return st;
+    if (inv_perm == nullptr) topk = 1;
+    st = check_pairs(Mc, topk, out_rows);
+    if (st) return st;
+    if (Mc == 0 || out_rows == 0) return MOE_OK;
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(scales);
+    REQUIRE_PTR(out);
+    if (inv_perm) REQUIRE_PTR(inv_perm);
+    const size_t values = (size_t)Mc * width;
+    st = check_outputs({{out, (size_t)out_rows * width * 2, "out"}},
+                       {{q, values, "q"}, {scales, values / 32, "scales"}, {inv_perm, (size_t)Mc * topk * 4, "inv_perm"}});
+    if (st) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_rows(q, scales, inv_perm, nullptr, Mc, width, topk, out, out_rows, nullptr, cus,
+                            static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_permute_rows(const uint16_t* x, const int32_t* inv_perm, const float* topk_weights, int64_t Mc, int32_t K,
+                     int32_t topk, uint16_t* out, int64_t out_rows, float* row_weights, void* stream) {
+    REQUIRE(K > 0 && K % 8 == 0 && K <= 65536, MOE_ERR_SHAPE, "K=%d is not a positive multiple of 8 up to 65536", K);
+    int st = check_pairs(Mc, topk, out_rows);
+    if (st) return st;
+    if (Mc == 0 || out_rows == 0) return MOE_OK;   // empty tensors have no address
+    REQUIRE((topk_weights == nullptr) == (row_weights == nullptr), MOE_ERR_INVALID_ARG,
+            "topk_weights and row_weights must both be given or both be NULL");
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(inv_perm);
+    REQUIRE_PTR(out);
+    if (row_weights) {
+        REQUIRE_PTR(topk_weights);
+        REQUIRE_PTR(row_weights);
+    }
+    const size_t p_b = (size_t)Mc * topk * 4;
+    st = check_outputs({{out, (size_t)out_rows * K * 2, "out"}, {row_weights, (size_t)out_rows * 4, "row_weights"}},
+                       {{x, (size_t)Mc * K * 2, "x"}, {inv_perm, p_b, "inv_perm"}, {topk_weights, p_b, "topk_weights"}});
+    if (st) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_rows(x, nullptr, inv_perm, topk_weights, Mc, K, topk, out, out_rows, row_weights, cus,
+                            static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_grouped_gemm_bf16_silu_mul(const uint16_t* a, const uint16_t* w13, const int32_t* expert_offsets,
+                                   const int32_t* counts, int32_t El, int64_t cap_rows, int32_t n, int32_t k_in,
+                                   int64_t rows_hint, uint16_t* act, void* h, uint8_t* h_scales, void* stream) {
+    int st = check_gated(expert_offsets, counts, El, cap_rows, n, k_in, h, h_scales);
+    if (st) return st;
+    if (cap_rows == 0) return MOE_OK;
+    REQUIRE_PTR(a);
+    REQUIRE_PTR(w13);
+    REQUIRE_PTR(act);
+    if (h) REQUIRE_PTR(h);
+    if (h_scales) REQUIRE_PTR(h_scales);
+    const size_t values = (size_t)cap_rows * n;
+    st = check_outputs({{act, values * 2, "act"}, {h, values * (h_scales ? 2 : 4), "h"}, {h_scales, values / 16, "h_scales"}},
+                       {{a, (size_t)cap_rows * k_in * 2, "a"},
+                        {w13, (size_t)El * 2 * n * k_in * 2, "w13"},
+                        {expert_offsets, ((size_t)El + 1) * 4, "expert_offsets"},
+                        {counts, (size_t)El * 4, "counts"}});
+    if (st) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_gemm_bf16_silu_mul(a, w13, expert_offsets, counts, El, cap_rows, n, k_in,
+                                          rows_hint > 0 ? rows_hint : cap_rows, act, h, h_scales, cus,
+                                          static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_grouped_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w2, const int32_t* expert_offsets,
+                                         const int32_t* counts, int32_t El, int64_t cap_rows, int32_t k_out,
+                                         int32_t n, int64_t rows_hint, const void* h, const uint8_t* h_scales,
+                                         const float* row_weights, uint16_t* dh, uint16_t* act, float* dots,
+                                         void* stream) {
+    int st = check_gated(expert_offsets, counts, El, cap_rows, n, k_out, h, h_scales);
+    if (st) return st;
+    if (cap_rows == 0) return MOE_OK;
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(w2);
+    REQUIRE_PTR(h);
+    REQUIRE_PTR(dh);
+    if (h_scales) REQUIRE_PTR(h_scales);
+    if (row_weights) REQUIRE_PTR(row_weights);
+    if (act) REQUIRE_PTR(act);
+    if (dots) REQUIRE_PTR(dots);
+    const size_t values = (size_t)cap_rows * n;
+    const bool in_place = h_scales == nullptr && dh == h;
+    st = check_outputs({{dh, values * 4, "dh"}, {act, values * 2, "act"}, {dots, (size_t)cap_rows * ((n + 63) / 64) * 4, "dots"}},
+                       {{in_place ? nullptr : h, values * (h_scales ? 2 : 4), "h"},
+                        {h_scales, values / 16, "h_scales"},
+                        {dy, (size_t)cap_rows * k_out * 2, "dy"},
+                        {w2, (size_t)El * n * k_out * 2, "w2"},
+                        {row_weights, (size_t)cap_rows * 4, "row_weights"},
+                        {expert_offsets, ((size_t)El + 1) * 4, "expert_offsets"},
+                        {counts, (size_t)El * 4, "counts"}});
+    if (st) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st) return st;
+    HIP_OK(moe::launch_gemm_bf16_dgrad_silu_mul(dy, w2, expert_offsets, counts, El, cap_rows, k_out, n,
+                                                rows_hint > 0 ? rows_hint : cap_rows, h, h_scales, row_weights, dh,
+                                                act, dots, cus, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+int moe_topk_weights_bwd(const float* dots, int32_t num_dots, int64_t rows, const int32_t* inv_perm, int64_t Mc,
+                         int32_t topk, float* dweights, void* stream) {
+    REQUIRE(num_dots >= 1 && num_dots <= 1024, MOE_ERR_SHAPE, "num_dots=%d outside [1,1024]", num_dots);
+    int st = check_pairs(Mc, topk, rows);
+    if (st) return st;
+    if (Mc == 0) return MOE_OK;
+    if (rows > 0) REQUIRE_PTR(dots);
+    REQUIRE_PTR(inv_perm);
+    REQUIRE_PTR(dweights);
+    const size_t p_b = (size_t)Mc * topk * 4;
+    st = check_outputs({{dweights, p_b, "dweights"}},
+                       {{dots, (size_t)rows * num_dots * 4, "dots"}, {inv_perm, p_b, "inv_perm"}});
+    if (st) return st;
+    st = check_device(nullptr);
+    if (st) return st;
+    HIP_OK(moe::launch_topk_weights_bwd(dots, num_dots, rows, inv_perm, Mc * topk, dweights,
+                                        static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

@@ -1,0 +1,177 @@
+// checkpoint.hip -- what a training step keeps of a forward call in 8 bits, and
+// the rows of the backward pass, on gfx950.
+//
+// A block of 32 values along a row has one scale, the least power of two that
+// brings its largest magnitude to e4m3's 448 or below (one byte, E8M0), and 32
+// e4m3 codes.  A power of two costs e4m3 no precision (it has its own
+// exponents) and makes code * scale a bf16 number exactly, so nothing is
+// rounded when a checkpoint is restored.
+//
+// All kernels here are bound by HBM.
+#include "moe_device.hpp"
+#include "moe_internal.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxBlocks = 1 << 20;   // a launch holds fewer than 2^32 threads
+
+// The largest of a lane's value over its quad of lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xb1, 0xf, 0xf, false));   // lanes 1 0 3 2
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, false));   // lanes 2 3 0 1
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
+    uint2 c;
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
+    c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, w, true);
+    return c;
+}
+
+__device__ __forceinline__ uint4 decode8(uint2 c, float scale) {
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        o[2 * i] = f32x2_to_bf16x2(lo[0] * scale, lo[1] * scale);
+        o[2 * i + 1] = f32x2_to_bf16x2(hi[0] * scale, hi[1] * scale);
+    }
+    return uint4{o[0], o[1], o[2], o[3]};
+}
+
+// Rows are whole blocks, so the matrix is one line of them: a lane takes eight
+// values, a quad of lanes a block, each thread kSets of its octets in flight.
+constexpr int kSets = 4;
+__global__ __launch_bounds__(kThreads) void k_encode(const uint16_t* __restrict__ x, int64_t octets,
+                                                     uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+    const int64_t stride = (int64_t)gridDim.x * kThreads * kSets;
+    for (int64_t o0 = (int64_t)blockIdx.x * kThreads * kSets + threadIdx.x; o0 < octets; o0 += stride) {
+        uint4 in[kSets];
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            const int64_t o = o0 + s * kThreads;
+            in[s] = load_once16(x + (o < octets ? o : o0) * 8);
+        }
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            const int64_t o = o0 + s * kThreads;   // of a quad, all four or none are below octets
+            float v[8];
+            bf16x8_to_f32(in[s], v);
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+            const uint32_t e = e8m0_of(quad_max(m));
+            if (o >= octets) break;
+            const uint2 c = encode8(v, e8m0_inverse(e));
+            *reinterpret_cast<uint2*>(q + o * 8) = c;
+            if ((threadIdx.x & 3) == 0) scales[o >> 2] = (uint8_t)e;
+        }
+    }
+}
+
+// out[inv_perm[t, k]] = token t's row, bf16 as it is or restored from 8 bits,
+// and row_weights[inv_perm[t, k]] = topk_w[t, k]; inv_perm null: out[t].  One
+// wave takes a token and a share of its picks and reads its row once for them,
+// kSlabs slabs of 512 columns at a time.
+template <bool CODES>
+__global__ __launch_bounds__(kThreads) void k_rows(const void* __restrict__ x, const uint8_t* __restrict__ scales,
+                                                   const int32_t* __restrict__ inv_perm,
+                                                   const float* __restrict__ topk_w, int64_t Mc, int K, int topk,
+                                                   uint16_t* __restrict__ out, int64_t out_rows,
+                                                   float* __restrict__ row_weights) {
+    constexpr int kSlabs = 4;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int per = (topk + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int k_lo = (int)blockIdx.y * per, k_end = min(topk, k_lo + per);
+    int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    for (; t < Mc; t += (int64_t)gridDim.x * (kThreads / kWave)) {
+        for (int c0 = lane * 8; c0 - lane * 8 < K; c0 += kSlabs * kWave * 8) {
+            uint4 v[kSlabs];
+            if constexpr (CODES) {
+                uint2 q[kSlabs];
+                uint32_t s[kSlabs];
+#pragma unroll
+                for (int b = 0; b < kSlabs; ++b) {
+                    const int64_t at = t * K + min(c0 + b * kWave * 8, K - 8);
+                    q[b] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(x) + at);
+                    s[b] = scales[at >> 5];
+                }
+#pragma unroll
+                for (int b = 0; b < kSlabs; ++b) v[b] = decode8(q[b], e8m0_value(s[b]));
+            } else {
+#pragma unroll
+                for (int b = 0; b < kSlabs; ++b)
+                    v[b] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + t * K +
+                                                           min(c0 + b * kWave * 8, K - 8));
+            }
+            for (int k = k_lo; k < k_end; ++k) {
+                const int64_t row = inv_perm ? inv_perm[t * topk + k] : t;
+                if (row < 0 || row >= out_rows) continue;
+#pragma unroll
+                for (int b = 0; b < kSlabs; ++b) {
+                    const int c = c0 + b * kWave * 8;
+                    if (c < K) *reinterpret_cast<uint4*>(out + row * K + c) = v[b];
+                }
+                if (row_weights && c0 == 0) row_weights[row] = topk_w[t * topk + k];
+            }
+        }
+    }
+}
+
+// dweights[t, k] = the sum of dots[inv_perm[t, k], :], sixteen lanes a pair, in
+// a fixed order.
+__global__ __launch_bounds__(kThreads) void k_dots(const float* __restrict__ dots, int nd, int64_t rows,
+                                                   const int32_t* __restrict__ inv_perm, int64_t pairs,
+                                                   float* __restrict__ dweights) {
+    const int l = threadIdx.x & 15;
+    for (int64_t p = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4; p < pairs;
+         p += (int64_t)gridDim.x * (kThreads / 16)) {
+        const int64_t row = inv_perm[p];
+        float sum = 0.0f;
+        if (row >= 0 && row < rows)
+            for (int i = l; i < nd; i += 16) sum += dots[row * nd + i];
+#pragma unroll
+        for (int m = 8; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 16);
+        if (l == 0) dweights[p] = sum;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_checkpoint(const uint16_t* x, int64_t values, uint8_t* q, uint8_t* scales, hipStream_t s) {
+    const int64_t octets = values / 8, per = kThreads * kSets;
+    int64_t b = (octets + per - 1) / per;
+    b = b < kMaxBlocks ? b : kMaxBlocks;
+    k_encode<<<(unsigned)b, kThreads, 0, s>>>(x, octets, q, scales);
+    return hipGetLastError();
+}
+
+// x: bf16 rows (scales null) or e4m3 codes
+hipError_t launch_rows(const void* x, const uint8_t* scales, const int32_t* inv_perm, const float* topk_w, int64_t Mc,
+                       int K, int topk, uint16_t* out, int64_t out_rows, float* row_weights, int num_cus,
+                       hipStream_t s) {
+    int64_t bx = (Mc + kThreads / kWave - 1) / (kThreads / kWave);
+    bx = bx < kMaxBlocks ? bx : kMaxBlocks;
+    // a token's picks over several waves until there are 8 blocks per CU
+    int64_t by = (8 * (int64_t)num_cus + bx - 1) / bx;
+    by = by > topk ? topk : by;
+    auto* k = scales ? k_rows<true> : k_rows<false>;
+    k<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, s>>>(x, scales, inv_perm, topk_w, Mc, K, topk, out, out_rows,
+                                                            row_weights);
+    return hipGetLastError();
+}
+
+hipError_t launch_topk_weights_bwd(const float* dots, int nd, int64_t rows, const int32_t* inv_perm, int64_t pairs,
+                                   float* dweights, hipStream_t s) {
+    int64_t b = (pairs + kThreads / 16 - 1) / (kThreads / 16);
+    b = b < kMaxBlocks ? b : kMaxBlocks;
+    k_dots<<<(unsigned)b, kThreads, 0, s>>>(dots, nd, rows, inv_perm, pairs, dweights);
+    return hipGetLastError();
+}
+
+}  // namespace moe

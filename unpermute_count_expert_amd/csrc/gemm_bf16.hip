@@ -80,7 +80,18 @@
 namespace moe {
 namespace {
 
-enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2, kGated = 3, kGatedBwd = 4 };
+enum { kKeepNone = 0, kKeepBf16 = 1, kKeepE4m3 = 2 };   // gate and up rows for the backward pass
+
+// What the gated products have besides: kGated writes h (and h_s), kGatedBwd
+// reads them and writes act and dots, where not null.
+struct Gate {
+    void* h;              // [cap_rows, 2 n] bf16 or e4m3
+    uint8_t* h_s;         // [cap_rows, 2 n / 32]
+    const float* row_w;   // [cap_rows]
+    float* dots;          // [cap_rows, ceil(n / 64)]
+    uint16_t* act;        // [cap_rows, n]
+};
 
 constexpr int BN = 256;
 constexpr int BK = 64;
@@ -199,6 +210,175 @@ __device__ __forceinline__ v4u pack_pair(const v4f& x, const v4f& y) {
     return v4u{w0[0], w1[0], w0[1], w1[1]};
 }
 
+// its inverse: eight bf16 as two column blocks' four values
+__device__ __forceinline__ void unpack_pair(const v4u& v, v4f& x, v4f& y) {
+    const auto w0 = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false);
+    const auto w1 = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
+    x = v4f{__uint_as_float(w0[0] << 16), __uint_as_float(w0[0] & 0xffff0000u), __uint_as_float(w1[0] << 16),
+            __uint_as_float(w1[0] & 0xffff0000u)};
+    y = v4f{__uint_as_float(w0[1] << 16), __uint_as_float(w0[1] & 0xffff0000u), __uint_as_float(w1[1] << 16),
+            __uint_as_float(w1[1] & 0xffff0000u)};
+}
+
+// ---- the gated products' epilogues ----------------------------------------------
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// silu(g) u
+__device__ __forceinline__ v4f gated(const v4f& g, const v4f& u) {
+    v4f a;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) a[q] = g[q] * sigmoid(g[q]) * u[q];
+    return a;
+}
+
+// the four lane rows' values of f, in every lane row
+template <typename F>
+__device__ __forceinline__ uint32_t over_lane_rows(uint32_t v, F f) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = f(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return f(b[0], b[1]);
+}
+
+// four fp32 as e4m3 codes times inv
+__device__ __forceinline__ uint32_t to_codes(const v4f& v, float inv) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
+}
+__device__ __forceinline__ v4f from_codes(uint32_t c, float scale) {
+    const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+    return v4f{lo[0] * scale, lo[1] * scale, hi[0] * scale, hi[1] * scale};
+}
+__device__ __forceinline__ uint32_t magnitude(const v4f& v) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(v[q]) & 0x7fffffffu);
+    return m;
+}
+
+// Backward through silu(g) u of four columns: d is the gradient of act, w the
+// row's weight.  act = w silu(g) u, dg and du the gradients of gate and up
+// times w; returns the sum of silu(g) u d.
+__device__ __forceinline__ float gated_bwd(const v4f& g, const v4f& u, const v4f& d, float w, v4f& act, v4f& dg,
+                                           v4f& du) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float s = sigmoid(g[q]), silu = g[q] * s, a = silu * u[q], wd = w * d[q];
+        dot = __builtin_fmaf(a, d[q], dot);
+        act[q] = w * a;
+        dg[q] = wd * u[q] * (s * (1.0f + g[q] * (1.0f - s)));
+        du[q] = wd * silu;
+    }
+    return dot;
+}
+
+// A descriptor of rows of `ld` bytes at p + at: `rows` of them, the last one
+// `last` bytes long.  Empty where that is negative, as it is for a unit past
+// the last column: the hardware takes the size as unsigned.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t at, int rows, int ld, int last) {
+    return __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t*>(const_cast<void*>(p)) + at, 0,
+                                             rows <= 0 ? 0 : max((rows - 1) * ld + last, 0), 0x00020000);
+}
+
+// What the backward epilogue reads of 16 rows by 64 columns from n0 on, a
+// lane its row (lane mod 16) and, in each half, its eight of 32 columns.
+template <int KEEP>
+struct GateIn {
+    v4u h[2][KEEP == kKeepBf16 ? 2 : 1];   // gate and up; codes: both in one
+    uint32_t scale;                        // lane rows: gate, gate, up, up of the two halves
+    float weight;
+    __device__ __forceinline__ void fetch(const Gate& gate, int N, int row0, int rows, int n0) {
+        constexpr int ks = KEEP == kKeepBf16 ? 2 : 1;
+        const int lane = threadIdx.x & (kWave - 1), rl = lane & 15, g = lane >> 4, c0 = 16 * (g & 1) + 8 * (g >> 1);
+        const int w = N - n0;
+        const auto r = rows_rsrc(gate.h, ((int64_t)row0 * 2 * N + n0) * ks, rows, 2 * N * ks, (N + w) * ks);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t at = c0 + 32 * p < w ? (uint32_t)((rl * 2 * N + c0 + 32 * p) * ks) : kNowhere;
+            if constexpr (KEEP == kKeepBf16) {
+                h[p][0] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kNonTemporal);
+                h[p][1] = __builtin_amdgcn_raw_buffer_load_b128(r, at + N * 2, 0, kNonTemporal);
+            } else {
+                const v2u gq = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+                const v2u uq = __builtin_amdgcn_raw_buffer_load_b64(r, at + N, 0, 0);
+                h[p][0] = v4u{gq[0], gq[1], uq[0], uq[1]};
+            }
+        }
+        if constexpr (KEEP == kKeepE4m3)
+            scale = __builtin_amdgcn_raw_buffer_load_b8(
+                rows_rsrc(gate.h_s, (int64_t)row0 * (N / 16) + n0 / 32, rows, N / 16, N / 32 + (w > 32 ? 2 : 1)),
+                (g & 1) * 32 < w ? (uint32_t)(rl * (N / 16) + (g & 1) + (g >> 1) * (N / 32)) : kNowhere, 0, 0);
+        weight = 1.0f;
+        if (gate.row_w)
+            weight = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(rows_rsrc(gate.row_w, (int64_t)row0 * 4, rows, 4, 4),
+                                                            (uint32_t)rl * 4, 0, 0));
+    }
+};
+
+// The backward epilogue of those rows and columns, whose gradient of act is in
+// d: writes dh, and act if wanted, and returns the lane's share of its row's
+// dot product.
+template <int KEEP>
+__device__ __forceinline__ float gated_bwd_rows(const Gate& gate, void* dh, int N, int row0, int rows, int n0,
+                                                const GateIn<KEEP>& in, const v4f (&d)[4]) {
+    const int lane = threadIdx.x & (kWave - 1), rl = lane & 15, g = lane >> 4, c0 = 16 * (g & 1) + 8 * (g >> 1);
+    const int w = N - n0;
+    float sc[2][2];   // [gate or up][half]
+    if constexpr (KEEP == kKeepE4m3) {
+        const auto a = __builtin_amdgcn_permlane32_swap(in.scale, in.scale, false, false);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto b = __builtin_amdgcn_permlane16_swap(a[i], a[i], false, false);
+            sc[i][0] = e8m0_value(b[0]);
+            sc[i][1] = e8m0_value(b[1]);
+        }
+    }
+    const auto rh = rows_rsrc(dh, ((int64_t)row0 * 2 * N + n0) * 2, rows, 4 * N, (N + w) * 2);
+    const auto ra = rows_rsrc(gate.act, ((int64_t)row0 * N + n0) * 2, rows, 2 * N, w * 2);
+    float dot = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        v4f gx, gy, ux, uy, act[2], dg[2], du[2];
+        if constexpr (KEEP == kKeepBf16) {
+            unpack_pair(in.h[p][0], gx, gy);
+            unpack_pair(in.h[p][1], ux, uy);
+        } else {
+            const auto gq = __builtin_amdgcn_permlane16_swap(in.h[p][0][0], in.h[p][0][1], false, false);
+            const auto uq = __builtin_amdgcn_permlane16_swap(in.h[p][0][2], in.h[p][0][3], false, false);
+            gx = from_codes(gq[0], sc[0][p]);
+            gy = from_codes(gq[1], sc[0][p]);
+            ux = from_codes(uq[0], sc[1][p]);
+            uy = from_codes(uq[1], sc[1][p]);
+        }
+        dot += gated_bwd(gx, ux, d[2 * p], in.weight, act[0], dg[0], du[0]);
+        dot += gated_bwd(gy, uy, d[2 * p + 1], in.weight, act[1], dg[1], du[1]);
+        const int c = c0 + 32 * p;
+        const uint32_t at = c < w ? (uint32_t)((rl * 2 * N + c) * 2) : kNowhere;
+        __builtin_amdgcn_raw_buffer_store_b128(pack_pair(dg[0], dg[1]), rh, at, 0, kNonTemporal);
+        __builtin_amdgcn_raw_buffer_store_b128(pack_pair(du[0], du[1]), rh, at + N * 2, 0, kNonTemporal);
+        if (gate.act)
+            __builtin_amdgcn_raw_buffer_store_b128(pack_pair(act[0], act[1]), ra,
+                                                   c < w ? (uint32_t)((rl * N + c) * 2) : kNowhere, 0, kNonTemporal);
+    }
+    return dot;
+}
+
+// the sum over the four lane rows, in every lane row
+__device__ __forceinline__ float row_sum(float v) {
+    return __uint_as_float(over_lane_rows(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+        return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+    }));
+}
+// and the largest
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    return over_lane_rows(v, [](uint32_t x, uint32_t y) { return max(x, y); });
+}
+
 // ---- k_tiles -----------------------------------------------------------------
 constexpr int kGran = 8192;   // a granule
 constexpr int kRing = 19;     // granules in the ring
@@ -227,13 +407,16 @@ struct Cursor {
 // the loads that a wave has issued after the one needed; they are exact,
 // because past the last tile the stream goes on with loads of zero bytes.
 // F32: fp32 outputs; ACC: added to what is there.
-template <int MODE, int NA, bool F32, bool ACC, bool TURN>   // TURN: forward only
+template <int MODE, int NA, bool F32, bool ACC, bool TURN, int KEEP>   // TURN: forward only; KEEP: gated only
 __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
                                                        const int32_t* __restrict__ offsets,
                                                        const int32_t* __restrict__ counts, int El, int64_t cap_rows,
-                                                       int n_out, int k_in, void* __restrict__ out) {
+                                                       int n_out, int k_in, void* out, Gate gate) {
+    constexpr bool GATED = MODE == kGated, FWD = MODE == kFwd || GATED, GBWD = MODE == kGatedBwd;
+    constexpr bool DG = MODE == kDgrad || GBWD;
+    constexpr int TN = GATED ? BN / 2 : BN;   // columns of a tile; GATED: of gate and of up
     constexpr int MI = 4 * NA, BM = 128 * NA, NJ = 4;
-    constexpr bool AT = MODE == kWgrad, BT = MODE != kFwd;   // column layout
+    constexpr bool AT = MODE == kWgrad, BT = !FWD;   // column layout
     constexpr int P = 2 * NA + 4, R = kRing % P;
     constexpr int kAhead = (kRing - NA - 4) / P;   // the step that the first even phase goes on loading
     static_assert(R <= 4 && (kRing - NA - 4) % P == R + NA, "the phases' shares of a step");
@@ -249,7 +432,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int grp = wave >> 2, wn = wave & 3;
-    const int N = MODE == kFwd ? n_out : k_in;   // output columns
+    const int N = FWD ? n_out : k_in;   // output columns
 
     // The experts in the order their tiles are walked, and, where they fit,
     // their rows.  Forward and dgrad: as they come, with the first m-tile of
@@ -334,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     // tiles the XCD's eighth, so that each has its share of the long ones
     // (4096 tokens on hot experts, 2048 x 768: 363 us in eighths, 165 dealt; 512
     // tokens, all short, 1536 x 2048, fp32: 253 and 263).
-    const int ntn = (N + BN - 1) / BN;
+    const int ntn = (N + TN - 1) / TN;
     const int xcd = blockIdx.x & 7, nslots = gridDim.x >> 3;
     const int64_t total = (int64_t)mtiles * ntn;
     const int64_t t_lo = alike ? total * xcd / 8 : xcd * nslots;
@@ -395,18 +578,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         return MODE == kWgrad ? c.tm * BM : c.lo + c.tm * BM;
     };
     auto depth = [&](const Cursor& c) __attribute__((always_inline)) {
-        return MODE == kFwd ? k_in : MODE == kDgrad ? n_out : c.hi - c.lo;
+        return FWD ? k_in : DG ? n_out : c.hi - c.lo;
     };
 
     // ---- the operand stream -------------------------------------------------
-    const int ldA = 2 * (MODE == kFwd ? k_in : n_out), ldB = 2 * k_in;   // bytes between rows in memory
+    const int ldA = 2 * (FWD ? k_in : n_out), ldB = 2 * k_in;   // bytes between rows in memory
     // A granule is eight kilobytes of eight rows; wave wn of a group moves
     // kilobytes 2 wn and 2 wn + 1, whose rows lie 8 * ld apart (and whose row
     // layout swaps neighbouring chunks).
     const int gr = wn * 16 + (lane >> 3);
     const int crow = swz(lane & 7, gr), ccol = ((((lane & 7) >> 1) ^ fx(gr)) << 1) | (lane & 1);
     const uint32_t voA = (uint32_t)(gr * ldA + (AT ? ccol : crow) * 16);
-    const uint32_t voB = MODE == kFwd ? voA : (uint32_t)(gr * ldB + (BT ? ccol : crow) * 16);
+    const uint32_t voB = FWD ? voA : (uint32_t)(gr * ldB + (BT ? ccol : crow) * 16);
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     Cursor d;
@@ -424,18 +607,22 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     const int nsteps = (k_in + BK - 1) / BK;
     int d_cnt = 0;            // TURN: the tile's steps left
     int d_q = 0;              // ring slot of the step's granule 0
-    const int gA = AT ? 128 : 64 * ldA, gB = BT ? 128 : 64 * ldB;   // bytes between granules in memory
+    const int gA = AT ? 128 : 64 * ldA, gB = BT ? 128 : GATED ? 32 * ldB : 64 * ldB;   // bytes between granules in memory
+    // GATED: a weight granule's rows 0..31 are gate rows (waves 0 and 1 of a
+    // group move them), 32..63 the same columns' up rows
+    const int up_rows = GATED && wn >= 2 ? 32 : 0;
     auto d_tile = [&]() __attribute__((always_inline)) {
-        const int m0 = m_first(d), n0 = d.tn * BN;
+        const int m0 = m_first(d), n0 = d.tn * TN;
         d_left = depth(d);
-        const int mrows = min((MODE == kWgrad ? n_out : d.hi) - m0, BM), ncols = min(N - n0, BN);
+        const int mrows = min((MODE == kWgrad ? n_out : d.hi) - m0, BM), ncols = min(N - n0, TN) + up_rows;
         tA = AT ? mrows * 2 : (mrows - 1) * ldA;
         tB = BT ? ncols * 2 : (ncols - 1) * ldB;
         const uint8_t* A = reinterpret_cast<const uint8_t*>(a);
         const uint8_t* B = reinterpret_cast<const uint8_t*>(b);
         dA = MODE == kWgrad ? A + (int64_t)d.lo * ldA + m0 * 2 : A + (int64_t)m0 * ldA;
-        dB = MODE == kFwd ? B + ((int64_t)d.x * n_out + n0) * ldB
-           : MODE == kDgrad ? B + (int64_t)d.x * n_out * ldB + n0 * 2
+        dB = GATED ? B + ((int64_t)d.x * 2 * n_out + n0 + (up_rows ? n_out - up_rows : 0)) * ldB
+           : FWD ? B + ((int64_t)d.x * n_out + n0) * ldB
+           : DG ? B + (int64_t)d.x * n_out * ldB + n0 * 2
                             : B + (int64_t)d.lo * ldB + n0 * 2;
         if constexpr (TURN) {
             d_cnt = nsteps;
@@ -564,7 +751,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         Part t;
         t.m0 = m_first(c) + grp * 64 * NA;
         t.m_end = MODE == kWgrad ? n_out : c.hi;
-        t.n0 = c.tn * BN + wn * 64;
+        t.n0 = c.tn * TN + wn * (TN / 4);
         t.e = c.x;
         t.mine = t.m0 < t.m_end && t.n0 < N;
         return t;
@@ -621,7 +808,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         return __builtin_bit_cast(v4f, whole ? __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kNonTemporal)
                                              : __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
     };
-    auto store = [&]() __attribute__((always_inline)) {
+    auto store_plain = [&]() __attribute__((always_inline)) {
         if (!done.mine) return;
         constexpr bool kLines = MODE == kWgrad;
         static_assert(!ACC || (kLines && F32), "accumulating: fp32 weight gradients");
@@ -676,6 +863,81 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
             sched_fence();
         }
     };
+    // GATED: a lane holds four columns of gate (blocks 0 and 1) and the same of
+    // up (2 and 3), so act needs no exchange between lanes, and a block of 32
+    // gate or up columns lies in one wave, whose four lane rows share its scale.
+    auto store_gated = [&]() __attribute__((always_inline)) {
+        if (!done.mine) return;
+        constexpr int ks = KEEP == kKeepBf16 ? 2 : 1;
+        const int rl = lane & 15, w = N - done.n0;
+        const uint32_t va = c0 < w ? (uint32_t)((rl * N + c0) * 2) : kNowhere;
+        const uint32_t vh = c0 < w ? (uint32_t)((rl * 2 * N + c0) * ks) : kNowhere;
+        uint32_t scale[2] = {0, 0};   // of gate and of up, a row block's in each lane row
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const v4f (&s)[NJ] = acc[i];
+            const int row0 = done.m0 + 16 * i, rows = done.m_end - row0;   // at least the block's; past the last one, none
+            __builtin_amdgcn_raw_buffer_store_b128(
+                pack_pair(gated(s[0], s[2]), gated(s[1], s[3])),
+                rows_rsrc(out, ((int64_t)row0 * N + done.n0) * 2, min(rows, 16), 2 * N, w * 2), va, 0, 0);
+            const auto rh = rows_rsrc(gate.h, ((int64_t)row0 * 2 * N + done.n0) * ks, min(rows, 16), 2 * N * ks, (N + w) * ks);
+            if constexpr (KEEP == kKeepBf16) {
+                __builtin_amdgcn_raw_buffer_store_b128(pack_pair(s[0], s[1]), rh, vh, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(pack_pair(s[2], s[3]), rh, vh + N * 2, 0, 0);
+            }
+            if constexpr (KEEP == kKeepE4m3) {
+                const auto rs = rows_rsrc(gate.h_s, (int64_t)(row0 - 16 * (i & 3)) * (N / 16) + done.n0 / 32,
+                                          min(rows + 16 * (i & 3), 64), N / 16, N / 32 + 1);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const v4f &x = s[2 * half], &y = s[2 * half + 1];
+                    const uint32_t e = e8m0_of(row_max(max(magnitude(x), magnitude(y))));
+                    const float inv = e8m0_inverse(e);
+                    const auto c = __builtin_amdgcn_permlane16_swap(to_codes(x, inv), to_codes(y, inv), false, false);
+                    __builtin_amdgcn_raw_buffer_store_b64(v2u{c[0], c[1]}, rh, vh + half * N, 0, 0);
+                    scale[half] = g == (i & 3) ? e : scale[half];
+                    if ((i & 3) == 3)   // four row blocks' scales at a time: lane l row l's
+                        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)scale[half], rs,
+                                                             (uint32_t)(lane * (N / 16) + half * (N / 32)), 0, 0);
+                }
+            }
+            sched_fence();
+        }
+    };
+    // GBWD: the gradient of act is in the sums; gate and up are read kAheadRows
+    // row blocks ahead of their use.
+    auto store_gated_bwd = [&]() __attribute__((always_inline)) {
+        if (!done.mine) return;
+        constexpr int kAheadRows = 3;
+        const int nd = (N + 63) / 64;
+        GateIn<KEEP> in[MI];
+        auto rows_from = [&](int i) __attribute__((always_inline)) { return done.m_end - done.m0 - 16 * i; };
+        auto fetch = [&](int i) __attribute__((always_inline)) {
+            in[i].fetch(gate, N, done.m0 + 16 * i, min(rows_from(i), 16), done.n0);
+        };
+#pragma unroll
+        for (int i = 0; i < kAheadRows; ++i) fetch(i);
+        float dots = 0.0f;   // a row block's in each lane row
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            if (i + kAheadRows < MI) fetch(i + kAheadRows);
+            const float dot = row_sum(gated_bwd_rows<KEEP>(gate, out, N, done.m0 + 16 * i, min(rows_from(i), 16), done.n0,
+                                                           in[i], acc[i]));
+            dots = g == (i & 3) ? dot : dots;
+            if (gate.dots && (i & 3) == 3)
+                __builtin_amdgcn_raw_buffer_store_b32(
+                    __float_as_uint(dots),
+                    rows_rsrc(gate.dots, ((int64_t)(done.m0 + 16 * (i - 3)) * nd + done.n0 / 64) * 4,
+                              min(rows_from(i - 3), 64), 4 * nd, 4),
+                    (uint32_t)(lane * 4 * nd), 0, 0);
+            sched_fence();
+        }
+    };
+    auto store = [&]() __attribute__((always_inline)) {
+        if constexpr (GATED) store_gated();
+        else if constexpr (GBWD) store_gated_bwd();
+        else store_plain();
+    };
     auto begin = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -723,7 +985,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
             v8bf fa[2][MI], fb[2][NJ];   // the step's fragments: dead between steps, where the stores need registers
             // (ACC: read whether they are used or not; else what the last step
             // left would pass for them, and the registers are taken in store())
-            if (ACC || t.mine) load(fa, fb);
+            if (ACC || GBWD || t.mine) load(fa, fb);
             if (!BT) puts();
             c_q = c_q + P >= kRing ? c_q + P - kRing : c_q + P;
             to_multiply();
@@ -745,15 +1007,16 @@ constexpr int kFewStages = 3;
 // (KS of the contraction each: 4 KB of weights and the rows' part).  MODE:
 // forward (row layouts, 32 columns) or dgrad (weights in column layout, 64
 // columns, so that a step still reads whole 128-byte lines).
-template <int MODE>
+template <int MODE, int KEEP>
 __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
                                                      const int32_t* __restrict__ offsets,
                                                      const int32_t* __restrict__ counts, int El, int64_t cap_rows,
-                                                     int n_out, int k_in, uint16_t* __restrict__ out) {
-    static_assert(MODE == kFwd || MODE == kDgrad, "the contraction is not the ragged axis");
-    constexpr bool BT = MODE == kDgrad;
+                                                     int n_out, int k_in, uint16_t* out, Gate gate) {
+    static_assert(MODE != kWgrad, "the contraction is not the ragged axis");
+    constexpr bool GATED = MODE == kGated, GBWD = MODE == kGatedBwd, FWD = MODE == kFwd || GATED, BT = !FWD;
     constexpr int NC = BT ? 64 : 32, KS = BT ? 32 : 64;
     constexpr int NJ = NC / 16, KK = KS / 32;
+    constexpr int TN = GATED ? NC / 2 : NC;   // columns of a unit; GATED: of gate and of up
     constexpr int kW = 4096, kStep = kW + 16 * KS * 2;        // a stage: weights, rows
     constexpr int kADma = 16 * KS * 2 / 1024, kDma = 4 + kADma;   // loads a step
     __shared__ __attribute__((aligned(1024))) uint8_t smem[kWaves * kFewStages * kStep];
@@ -763,13 +1026,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int uw = wave >> 2, kw = wave & 3;
-    const int N = MODE == kFwd ? n_out : k_in, C = MODE == kFwd ? k_in : n_out;
+    const int N = FWD ? n_out : k_in, C = FWD ? k_in : n_out;
     int lo2[2], hi2[2], nt[2];
     segments(offsets, counts, cap_rows, El, tid, lo2, hi2);
 #pragma unroll
     for (int j = 0; j < 2; ++j) nt[j] = (hi2[j] - lo2[j] + 15) / 16;
     const int tiles = expert_prefix(nt, El, cap_rows / 16 + El, s_tpre, reinterpret_cast<int64_t*>(smem));
-    const int ncu = (N + NC - 1) / NC;
+    // GATED: an even number, so that a block's two units are halves of the same 32 columns
+    const int ncu = GATED ? (N + 2 * TN - 1) / (2 * TN) * 2 : (N + TN - 1) / TN;
     const int64_t units = (int64_t)tiles * ncu;
     const int64_t first = 2 * (int64_t)blockIdx.x, stride = 2 * (int64_t)gridDim.x;
     if (first >= units) return;
@@ -783,7 +1047,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
         Unit x = {0, 0, 0, 0};
         if (u >= units) return x;
         const int t = (int)(u / ncu);
-        x.n0 = (int)(u - (int64_t)t * ncu) * NC;
+        x.n0 = (int)(u - (int64_t)t * ncu) * TN;
         int at = 0;   // experts whose first tile is not after t
         for (int j = 0; j < El; j += kWave)
             at += __popcll(ballot(j + lane < El && s_tpre[min(j + lane, El - 1)] <= t));
@@ -811,16 +1075,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
     auto issue = [&]() __attribute__((always_inline)) {
         const int k0 = (kw + 4 * d_j) * KS, left = d.rows > 0 ? C - k0 : 0;
         const uint32_t at = ring + d_slot * kStep;
-        const uint8_t* W = reinterpret_cast<const uint8_t*>(b) + (int64_t)d.e * n_out * ldB +
+        const uint8_t* W = reinterpret_cast<const uint8_t*>(b) + (int64_t)d.e * (GATED ? 2 * n_out : n_out) * ldB +
                            (BT ? (int64_t)k0 * ldB + d.n0 * 2 : (int64_t)d.n0 * ldB + k0 * 2);
         const int wb = left <= 0 ? 0 : BT ? (min(left, KS) - 1) * ldB + (N - d.n0) * 2
-                                          : (min(N - d.n0, NC) - 1) * ldB + left * 2;
+                                          : (min(N - d.n0, TN) - 1) * ldB + left * 2;
+        const int64_t up = GATED ? (int64_t)(n_out - TN) * ldB : 0;   // GATED: kilobytes 2 and 3 are up rows
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             // the next eight rows swap neighbouring chunks (row layout) or pairs of slots (column layout)
             uint32_t v = voB + ((h & 1) == 0 ? 0 : BT ? 64 - ((cB & 4) << 5) : 16 - ((cB & 1) << 5));
             if (!BT && left < KS) v |= (cB ^ (h & 1)) * 8 >= left ? kNowhere : 0u;
-            dma16(W + h * 8 * ldB, wb - h * 8 * ldB, v, at + h * 1024);
+            dma16(W + h * 8 * ldB + (h >= 2 ? up : 0), wb - (GATED ? h & 1 : h) * 8 * ldB, v, at + h * 1024);
         }
         const uint8_t* A = reinterpret_cast<const uint8_t*>(a) + (int64_t)d.m0 * ldA + k0 * 2;
         const int ab = left <= 0 ? 0 : (d.rows - 1) * ldA + left * 2;
@@ -884,12 +1149,45 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (kw == 0) {
             const Unit x = unit_of(u);
+            GateIn<KEEP> in;   // GBWD
+            if constexpr (GBWD) in.fetch(gate, N, x.m0, x.rows, x.n0);
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int w = 0; w < 3; ++w)
                     acc[j] += *reinterpret_cast<const v4f*>(&s_red[uw][w][(j * kWave + lane) * 4]);
             const int w = N - x.n0;   // columns from n0 on
+            if constexpr (GATED) {
+                const int rl = lane & 15;
+                const uint32_t c = (uint32_t)(4 * g);
+                const v4f a = gated(acc[0], acc[1]);
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    v2u{f32x2_to_bf16x2(a[0], a[1]), f32x2_to_bf16x2(a[2], a[3])},
+                    rows_rsrc(out, ((int64_t)x.m0 * N + x.n0) * 2, x.rows, 2 * N, w * 2),
+                    (int)c < w ? (rl * N + c) * 2 : kNowhere, 0, 0);
+                if constexpr (KEEP == kKeepBf16) {
+                    const auto rh = rows_rsrc(gate.h, ((int64_t)x.m0 * 2 * N + x.n0) * 2, x.rows, 4 * N, (N + w) * 2);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            v2u{f32x2_to_bf16x2(acc[j][0], acc[j][1]), f32x2_to_bf16x2(acc[j][2], acc[j][3])}, rh,
+                            (int)c < w ? (rl * 2 * N + c + j * N) * 2 : kNowhere, 0, 0);
+                }
+                if constexpr (KEEP == kKeepE4m3) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t m = row_max(magnitude(acc[j]));
+                        if (g == 0) s_red[uw][0][j * 16 + rl] = __uint_as_float(m);   // its sums are read
+                    }
+                }
+            } else if constexpr (GBWD) {
+                const int nd = (N + 63) / 64;
+                const float dot = row_sum(gated_bwd_rows<KEEP>(gate, out, N, x.m0, x.rows, x.n0, in, acc));
+                if (gate.dots)
+                    __builtin_amdgcn_raw_buffer_store_b32(
+                        __float_as_uint(dot), rows_rsrc(gate.dots, ((int64_t)x.m0 * nd + x.n0 / 64) * 4, x.rows, 4 * nd, 4),
+                        lane < 16 ? (uint32_t)(lane * 4 * nd) : kNowhere, 0, 0);
+            } else {
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
                 out + (int64_t)x.m0 * N + x.n0, 0, x.rows > 0 ? ((x.rows - 1) * N + w) * 2 : 0, 0x00020000);
 #pragma unroll
@@ -897,6 +1195,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
                 const int c = 32 * p + 16 * (g & 1) + 8 * (g >> 1);
                 const uint32_t v = c < w ? (uint32_t)(((lane & 15) * N + c) * 2) : kNowhere;
                 __builtin_amdgcn_raw_buffer_store_b128(pack_pair(acc[2 * p], acc[2 * p + 1]), r, v, 0, 0);
+            }
+            }
+        }
+        if constexpr (GATED && KEEP == kKeepE4m3) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // both units' maxima
+            if (kw == 0) {   // the block of 32 columns has the larger one's scale
+                const Unit x = unit_of(u);
+                const int rl = lane & 15;
+                const auto rh = rows_rsrc(gate.h, (int64_t)x.m0 * 2 * N + x.n0, x.rows, 2 * N, 2 * N - x.n0);
+                const auto rs = rows_rsrc(gate.h_s, (int64_t)x.m0 * (N / 16) + x.n0 / 32, x.rows, N / 16, N / 32 + 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t e = e8m0_of(max(__float_as_uint(s_red[0][0][j * 16 + rl]), __float_as_uint(s_red[1][0][j * 16 + rl])));
+                    __builtin_amdgcn_raw_buffer_store_b32(to_codes(acc[j], e8m0_inverse(e)), rh,
+                                                          (uint32_t)(rl * 2 * N + j * N + 4 * g), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b8(
+                        (uint8_t)e, rs, uw == 0 && g == 0 ? (uint32_t)(rl * (N / 16) + j * (N / 32)) : kNowhere, 0, 0);
+                }
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // s_red may be written again
@@ -933,28 +1249,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 // 128 rows, 59 with 256; 128 of 264 x 360, 16384 rows: 63 and 86; 128 of
 // 1536 x 2048, 32768 rows, bf16: 340 and 288).
 // Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
-template <int MODE, bool F32, bool ACC>
+template <int MODE, bool F32, bool ACC, int KEEP = kKeepNone>
 hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
-                  int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, void* out, int num_cus, hipStream_t s) {
+                  int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, void* out, int num_cus, hipStream_t s,
+                  Gate gate = {}) {
+    constexpr bool FWD = MODE == kFwd || MODE == kGated;
     const unsigned grid = (unsigned)((num_cus + 7) / 8 * 8);   // the same number of blocks on each of the eight XCDs
     auto tiles = [&](auto* kernel) {
-        kernel<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, out);
+        kernel<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, out, gate);
     };
     const double cus = num_cus;
-    const int ntn = ((MODE == kFwd ? n_out : k_in) + BN - 1) / BN;   // n-tiles
+    const int N = (FWD ? n_out : k_in) * (MODE == kGated ? 2 : 1);   // output columns; gate and up
+    const int ntn = (N + BN - 1) / BN;                               // n-tiles
     if constexpr (MODE == kWgrad) {
         const double rounds1 = std::ceil((double)El * ((n_out + 127) / 128) * ntn / cus);
         const double rounds2 = std::ceil((double)El * ((n_out + 255) / 256) * ntn / cus);
-        if (3 * rounds1 <= 5 * rounds2) tiles(k_tiles<MODE, 1, F32, ACC, false>);
-        else tiles(k_tiles<MODE, 2, F32, ACC, false>);
+        if (3 * rounds1 <= 5 * rounds2) tiles(k_tiles<MODE, 1, F32, ACC, false, KEEP>);
+        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP>);
     } else {
-        constexpr int NC = MODE == kDgrad ? 64 : 32, KS = MODE == kDgrad ? 32 : 64;   // k_few's columns and step
-        const int N = MODE == kFwd ? n_out : k_in, C = MODE == kFwd ? k_in : n_out;
+        constexpr int NC = FWD ? 32 : 64, KS = FWD ? 64 : 32;   // k_few's columns and step
+        const int C = FWD ? k_in : n_out;
         const double experts = rows_hint < El ? (double)rows_hint : El, r = (double)rows_hint / experts;
         const double bytes = experts * N * C * 2 / 5.5e6;   // the weights' time
         const double units = experts * std::max(1.0, r / 16 + 0.75) * ((N + NC - 1) / NC) / (2 * cus);
         const double few = 3.5 + std::max(1.0, units) *
-                                     (1.5 + (MODE == kDgrad ? 1.2 : 0.85) * ((C + 4 * KS - 1) / (4 * KS)));
+                                     (1.5 + (FWD ? 0.85 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
         // rounds of tiles; 128 rows unless 256 save more than a fifth of them
         const double rounds1 = experts * std::max(1.0, r / 128 + 0.5) * ntn / cus;
         const double rounds2 = experts * std::max(1.0, r / 256 + 0.5) * ntn / cus;
@@ -962,11 +1281,11 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
         const double walk = 6.5 + std::max(1.0, low ? rounds1 : rounds2) *
                                       (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
         if (std::max(few, bytes) <= std::max(walk, bytes + 1))
-            k_few<MODE><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
-                                                  static_cast<uint16_t*>(out));
-        else if (low) tiles(k_tiles<MODE, 1, F32, ACC, MODE == kFwd>);
-        else if (MODE == kFwd && rows_hint < (int64_t)208 * El) tiles(k_tiles<MODE, 2, F32, ACC, MODE == kFwd>);
-        else tiles(k_tiles<MODE, 2, F32, ACC, false>);
+            k_few<MODE, KEEP><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
+                                                        static_cast<uint16_t*>(out), gate);
+        else if (low) tiles(k_tiles<MODE, 1, F32, ACC, FWD, KEEP>);
+        else if (FWD && rows_hint < (int64_t)208 * El) tiles(k_tiles<MODE, 2, F32, ACC, FWD, KEEP>);
+        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP>);
     }
     return hipGetLastError();
 }
@@ -987,7 +1306,24 @@ hipError_t launch_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const i
                                   const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
                                   bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s) {
     auto* go = !f32 ? launch<kWgrad, false, false> : accumulate ? launch<kWgrad, true, true> : launch<kWgrad, true, false>;
-    return go(dy, a, offsets, counts, El, cap_rows, n_out, k_in, /*rows_hint=*/0, dw, num_cus, s);
+    return go(dy, a, offsets, counts, El, cap_rows, n_out, k_in, /*rows_hint=*/0, dw, num_cus, s, {});
+}
+hipError_t launch_gemm_bf16_silu_mul(const uint16_t* a, const uint16_t* w13, const int32_t* offsets,
+                                     const int32_t* counts, int El, int64_t cap_rows, int n, int k_in,
+                                     int64_t rows_hint, uint16_t* act, void* h, uint8_t* h_s, int num_cus,
+                                     hipStream_t s) {
+    auto* go = !h ? launch<kGated, false, false, kKeepNone>
+               : h_s ? launch<kGated, false, false, kKeepE4m3> : launch<kGated, false, false, kKeepBf16>;
+    return go(a, w13, offsets, counts, El, cap_rows, n, k_in, rows_hint, act, num_cus, s,
+              Gate{h, h_s, nullptr, nullptr, nullptr});
+}
+hipError_t launch_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w2, const int32_t* offsets,
+                                           const int32_t* counts, int El, int64_t cap_rows, int k_out, int n,
+                                           int64_t rows_hint, const void* h, const uint8_t* h_s, const float* row_w,
+                                           uint16_t* dh, uint16_t* act, float* dots, int num_cus, hipStream_t s) {
+    auto* go = h_s ? launch<kGatedBwd, false, false, kKeepE4m3> : launch<kGatedBwd, false, false, kKeepBf16>;
+    return go(dy, w2, offsets, counts, El, cap_rows, k_out, n, rows_hint, dh, num_cus, s,
+              Gate{const_cast<void*>(h), const_cast<uint8_t*>(h_s), row_w, dots, act});
 }
 
 }  // namespace moe

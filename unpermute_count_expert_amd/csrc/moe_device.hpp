@@ -122,6 +122,19 @@ __device__ __forceinline__ float quant_group16(const float (&x)[8], uint2& codes
     return scale;
 }
 
+// The scale of 32 values in 8 bits (E8M0: byte b stands for 2^(b - 127)): the
+// least power of two that brings the largest magnitude, as fp32 bits m, to 448
+// (1.75 * 2^8) or below, but at least 2^-117, so that every restored value is
+// a normal number in bf16, and 255 (NaN) where m is an infinity or a NaN.
+__device__ __forceinline__ uint32_t e8m0_of(uint32_t m) {
+    const int e = (int)((m + 0x1fffffu) >> 23) - 8;
+    return m >= 0x7f800000u ? 255u : (uint32_t)max(e, 10);
+}
+// 1 / its value, exact; for 255 an infinity, with which every value of the
+// block becomes the NaN code (0 included)
+__device__ __forceinline__ float e8m0_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+__device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b << 23 | (b == 255u ? 1u : 0u)); }
+
 // eight bf16 values (one 16-byte load) as fp32
 __device__ __forceinline__ void bf16x8_to_f32(uint4 u, float (&v)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};

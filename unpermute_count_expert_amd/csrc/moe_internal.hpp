@@ -167,6 +167,16 @@ hipError_t launch_gemm_bf16_dgrad(const uint16_t* dy, const uint16_t* w, const i
 hipError_t launch_gemm_bf16_wgrad(const uint16_t* dy, const uint16_t* a, const int32_t* offsets,
                                   const int32_t* counts, int El, int64_t cap_rows, int n_out, int k_in,
                                   bool f32, bool accumulate, void* dw, int num_cus, hipStream_t s);
+// The gate and up products with SiLU-mul (h null, bf16, or e4m3 with h_s), and
+// the down product's gradient by the rows through it.
+hipError_t launch_gemm_bf16_silu_mul(const uint16_t* a, const uint16_t* w13, const int32_t* offsets,
+                                     const int32_t* counts, int El, int64_t cap_rows, int n, int k_in,
+                                     int64_t rows_hint, uint16_t* act, void* h, uint8_t* h_s, int num_cus,
+                                     hipStream_t s);
+hipError_t launch_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w2, const int32_t* offsets,
+                                           const int32_t* counts, int El, int64_t cap_rows, int k_out, int n,
+                                           int64_t rows_hint, const void* h, const uint8_t* h_s, const float* row_w,
+                                           uint16_t* dh, uint16_t* act, float* dots, int num_cus, hipStream_t s);
 
 hipError_t launch_silu_mul(const uint16_t* h, int64_t rows, int n, const int32_t* offsets, const int32_t* counts,
                            int El, uint16_t* act, int num_cus, hipStream_t s);
@@ -176,6 +186,16 @@ hipError_t launch_silu_mul_bwd(const uint16_t* h, const uint16_t* dact, int64_t 
 hipError_t launch_unpermute_bwd(const uint16_t* dout, const uint16_t* y, int64_t y_rows, const int32_t* inv_perm,
                                 const float* topk_w, int64_t Mc, int K, int topk, uint16_t* dy, float* dweights,
                                 int num_cus, hipStream_t s);
+
+// 8-bit checkpoints (values a multiple of 32), rows in expert order from bf16
+// (scales null) or from 8 bits, and the router weights' gradient from the
+// gated backward pass's dot products.
+hipError_t launch_checkpoint(const uint16_t* x, int64_t values, uint8_t* q, uint8_t* scales, hipStream_t s);
+hipError_t launch_rows(const void* x, const uint8_t* scales, const int32_t* inv_perm, const float* topk_w, int64_t Mc,
+                       int K, int topk, uint16_t* out, int64_t out_rows, float* row_weights, int num_cus,
+                       hipStream_t s);
+hipError_t launch_topk_weights_bwd(const float* dots, int nd, int64_t rows, const int32_t* inv_perm, int64_t pairs,
+                                   float* dweights, hipStream_t s);
 
 // Tensors of one launch of the gradient kernels, whose sum of squares leaves
 // at most kGradBlocks partial sums.

@@ -86,6 +86,22 @@ class SavedRows:
     rows_hint: int
 
 
+@dataclass
+class SavedCheckpoint:
+    """The same where the layer keeps a checkpoint: the tokens (the caller's own tensor, which stays as it is until
+    then, or codes with their scales x_s) and the experts' gate and up rows (bf16, or codes with h_s)."""
+    tokens: int
+    topk_weights: torch.Tensor
+    counts: torch.Tensor
+    expert_offsets: torch.Tensor
+    inv_perm: torch.Tensor
+    x: torch.Tensor
+    x_s: Optional[torch.Tensor]
+    h: torch.Tensor
+    h_s: Optional[torch.Tensor]
+    rows_hint: int
+
+
 class MoeTrainLayer:
     """One GPU's local experts in bf16, forward and backward.
 
@@ -97,6 +113,21 @@ class MoeTrainLayer:
     clip_gradients() scales them in place to a global norm.  Every step is a
     library call on the current stream.  N and K: multiples of 128.
 
+    checkpoint: what a forward call keeps of its rows for backward().
+      None    the permuted tokens, gate and up rows, activations and expert
+              outputs in bf16, 4 K + 6 N bytes a row;
+      "bf16"  gate and up rows, 4 N bytes a row, and the caller's tokens;
+      "e4m3"  gate and up rows, 2 N bytes a row, and the tokens, K bytes
+              each, in 8 bits with a scale byte for every 32 values.
+    With a checkpoint the gate and up products and the activation are one
+    kernel, as are the down product's gradient and the activation's, which
+    recomputes the activations; the router weights' gradient comes from the
+    down product's gradient instead of its outputs.  8 bits round what the
+    gradients are taken at by up to 2^-4 of each value; the output is the same
+    with either checkpoint.
+
+    infer() is the forward pass alone: it keeps nothing.
+
     With gradients enabled and any of tokens, router weights and expert
     weights requiring them, forward()'s output carries a graph whose backward
     is backward(): the tokens and router weights get their gradients through
@@ -105,7 +136,10 @@ class MoeTrainLayer:
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, num_global_experts: int,
-                 expert_map: Optional[torch.Tensor] = None, align: int = 16):
+                 expert_map: Optional[torch.Tensor] = None, align: int = 16, checkpoint: Optional[str] = None):
+        if checkpoint not in (None, "bf16", "e4m3"):
+            raise ValueError(f"checkpoint is {checkpoint!r}; expected None, 'bf16' or 'e4m3'")
+        self.checkpoint = checkpoint
         bf = (torch.bfloat16,)
         _lib.check_arg(w13, "w13", bf, (None, None, None))
         self.El, twoN, self.K = w13.shape
@@ -135,20 +169,56 @@ class MoeTrainLayer:
 
     def forward(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor):
         """(out [M, K] bf16, the rows backward() needs)."""
-        _lib.check_arg(x, "x", (torch.bfloat16,), (None, self.K))
-        _lib.check_arg(topk_ids, "topk_ids", _lib.I32, (x.shape[0], None))
-        _lib.check_arg(topk_weights, "topk_weights", _lib.F32, topk_ids.shape)
-        _lib.check_device(x, topk_ids, topk_weights, self.w13)
+        self._check_tokens(x, topk_ids, topk_weights)
         if torch.is_grad_enabled():
             weights = self.w13.requires_grad or self.w2.requires_grad
             if weights or x.requires_grad or topk_weights.requires_grad:
                 return _Graph.apply(x, topk_weights, _anchor() if weights else None, topk_ids, self)
         return self._forward(x, topk_ids, topk_weights)
 
+    def infer(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor) -> torch.Tensor:
+        """The output [M, K] bf16 of a forward call with a checkpoint, none kept and no graph."""
+        self._check_tokens(x, topk_ids, topk_weights)
+        return self._gated_forward(x, topk_ids, topk_weights, None, None)[0]
+
+    def _check_tokens(self, x, topk_ids, topk_weights):
+        _lib.check_arg(x, "x", (torch.bfloat16,), (None, self.K))
+        _lib.check_arg(topk_ids, "topk_ids", _lib.I32, (x.shape[0], None))
+        _lib.check_arg(topk_weights, "topk_weights", _lib.F32, topk_ids.shape)
+        _lib.check_device(x, topk_ids, topk_weights, self.w13)
+
+    def _gated_forward(self, x, topk_ids, topk_weights, h, h_s):
+        """(out, counts, expert_offsets, inv_perm, rows_hint), with gate and up rows kept in h and h_s if given."""
+        M, topk = topk_ids.shape
+        El, K, N, i32 = self.El, self.K, self.N, torch.int32
+        cap = _lib.moe_max_rows(M, topk, El, self.align)
+        hint = max(1, M * topk * El // self.Eg)
+        counts, offsets, inv = (self._empty(*n, dtype=i32) for n in ((El,), (El + 1,), (M, topk)))
+        a, act = self._empty(cap, K), self._empty(cap, N)
+        ws = self._empty(_lib.moe_permute_workspace_size(M, topk, El), dtype=torch.uint8)
+        _lib.moe_permute_bf16(x, topk_ids, self.expert_map, self.Eg, El, self.align, cap, a, counts, offsets, inv,
+                              self._empty(cap, dtype=i32), ws)
+        _lib.moe_grouped_gemm_bf16_silu_mul(a, self.w13, offsets, counts, act, h, h_s, hint)
+        _lib.moe_grouped_gemm_bf16(act, self.w2, offsets, counts, a, hint)   # the experts' outputs, in the tokens' place
+        out = self._empty(M, K)
+        _lib.moe_unpermute_weight_reduce(a, inv, topk_weights, 0, out)
+        return out, counts, offsets, inv, hint
+
     def _forward(self, x, topk_ids, topk_weights):
         M, topk = topk_ids.shape
         El, K, N, i32 = self.El, self.K, self.N, torch.int32
         cap = _lib.moe_max_rows(M, topk, El, self.align)
+        if self.checkpoint is not None:
+            h_s = x_s = None
+            if self.checkpoint == "e4m3":
+                u8, block = torch.uint8, _lib.CHECKPOINT_BLOCK
+                h, h_s = self._empty(cap, 2 * N, dtype=u8), self._empty(cap, 2 * N // block, dtype=u8)
+                kept, x_s = self._empty(M, K, dtype=u8), self._empty(M, K // block, dtype=u8)
+                _lib.moe_checkpoint(x, kept, x_s)
+            else:
+                h, kept = self._empty(cap, 2 * N), x
+            out, counts, offsets, inv, hint = self._gated_forward(x, topk_ids, topk_weights, h, h_s)
+            return out, SavedCheckpoint(M, topk_weights, counts, offsets, inv, kept, x_s, h, h_s, hint)
         s = SavedRows(M, topk_weights, self._empty(El, dtype=i32), self._empty(El + 1, dtype=i32),
                       self._empty(M, topk, dtype=i32), self._empty(cap, K), self._empty(cap, 2 * N),
                       self._empty(cap, N), self._empty(cap, K), max(1, M * topk * El // self.Eg))
@@ -163,10 +233,12 @@ class MoeTrainLayer:
         _lib.moe_unpermute_weight_reduce(s.y, s.inv_perm, topk_weights, 0, out)
         return out, s
 
-    def backward(self, dout: torch.Tensor, s: SavedRows):
+    def backward(self, dout: torch.Tensor, s):
         """(dx [M, K] bf16, gradient of topk_weights [M, topk] fp32); adds to grad_w13 and grad_w2."""
         _lib.check_arg(dout, "dout", (torch.bfloat16,), (s.tokens, self.K))
         _lib.check_device(dout, self.w13)
+        if isinstance(s, SavedCheckpoint):
+            return self._backward_checkpoint(dout, s)
         El, N = self.El, self.N
         seg = (s.expert_offsets, s.counts)
         dy, dweights = torch.empty_like(s.y), torch.empty_like(s.topk_weights)
@@ -180,6 +252,28 @@ class MoeTrainLayer:
         _lib.moe_grouped_gemm_bf16_dgrad(dh, self.w13, *seg, da, s.rows_hint)
         # a token's row was copied to each of its experts: its gradient is the plain sum of theirs
         _lib.moe_unpermute_weight_reduce(da, s.inv_perm, None, 1, dx)
+        return dx, dweights
+
+    def _backward_checkpoint(self, dout, s):
+        K, N, f32 = self.K, self.N, torch.float32
+        cap = s.h.shape[0]
+        seg = (s.expert_offsets, s.counts)
+        d, weights = self._empty(cap, K), self._empty(cap, dtype=f32)
+        _lib.moe_permute_rows(dout, s.inv_perm, d, s.topk_weights, weights)
+        dh, act, dots = self._empty(cap, 2 * N), self._empty(cap, N), self._empty(cap, -(-N // 64), dtype=f32)
+        _lib.moe_grouped_gemm_bf16_dgrad_silu_mul(d, self.w2, *seg, s.h, dh, act, s.h_s, weights, dots, s.rows_hint)
+        dweights = torch.empty_like(s.topk_weights)
+        _lib.moe_topk_weights_bwd(dots, s.inv_perm, dweights)
+        _lib.moe_grouped_gemm_bf16_wgrad(d, act, *seg, self.grad_w2, 1, s.rows_hint)   # act has the router weights
+        a = self._empty(cap, K)
+        if s.x_s is None:
+            _lib.moe_permute_rows(s.x, s.inv_perm, a)
+        else:
+            _lib.moe_checkpoint_restore(s.x, s.x_s, a, s.inv_perm)
+        _lib.moe_grouped_gemm_bf16_wgrad(dh, a, *seg, self.grad_w13, 1, s.rows_hint)
+        dx = torch.empty_like(dout)
+        _lib.moe_grouped_gemm_bf16_dgrad(dh, self.w13, *seg, d, s.rows_hint)   # d is read: its rows' gradients
+        _lib.moe_unpermute_weight_reduce(d, s.inv_perm, None, 1, dx)
         return dx, dweights
 
     def clip_gradients(self, max_norm: float, extra=(), reduce=None) -> torch.Tensor:
@@ -210,7 +304,8 @@ class _Graph(torch.autograd.Function):
     def forward(ctx, x, topk_weights, anchor, topk_ids, layer):
         out, ctx.rows = layer._forward(x, topk_ids, topk_weights)
         ctx.layer = layer
-        ctx.save_for_backward(topk_weights, layer.w13.detach(), layer.w2.detach())
+        kept = (x,) if layer.checkpoint == "bf16" else ()
+        ctx.save_for_backward(topk_weights, layer.w13.detach(), layer.w2.detach(), *kept)
         return out, ctx.rows
 
     @staticmethod
