@@ -446,8 +446,7 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
  * 448 or below, but at least 2^-117; codes are rounded to nearest even, so a
  * value is off by at most 2^-4 of itself, or 2^-10 of the scale if that is
  * more.  A block that holds an infinity or a NaN has b = 255 and is NaN
- * throughout.  What is restored is exact in bf16.  b = 0, never written, reads
- * as 0. */
+ * throughout.  What is restored is exact in bf16. */
 
 /* x [rows,width] bf16 -> codes q [rows,width], scales [rows,width/32].
  * width: positive multiple of 32 up to 65536. */

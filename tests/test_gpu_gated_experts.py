@@ -454,3 +454,14 @@ def test_gated_many_experts():
             v, tol = bwd_reference(ref, a[r].double() @ w2[e].double(), torch.zeros(cs[e], n, dtype=F64),
                                    torch.ones(cs[e], dtype=F64), n)["dg"]
             within(dh[r, :n], v, tol + 2.0 ** -8 * (v.abs() + tol) + TINY, "dg")
+
+
+def test_restore_every_code_and_scale():
+    """Every code with every scale byte, subnormal values among them, restored dense."""
+    q = torch.arange(256, dtype=torch.int16).to(U8).repeat(256, 1)
+    s = torch.arange(256, dtype=torch.int16).to(U8)[:, None].repeat(1, 8)
+    out = sentinel((256, 256))
+    moe.moe_checkpoint_restore(q.to(DEV), s.to(DEV), out)
+    want = decode(q, s)
+    within(out.cpu().double().nan_to_num(12345.0), want.float().to(BF).double().nan_to_num(12345.0), torch.zeros(()), "restored")
+    assert torch.equal(torch.isnan(out.cpu()), torch.isnan(want))

@@ -37,9 +37,10 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float scale) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-        o[2 * i] = f32x2_to_bf16x2(lo[0] * scale, lo[1] * scale);
-        o[2 * i + 1] = f32x2_to_bf16x2(hi[0] * scale, hi[1] * scale);
+        const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], scale, false);
+        const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], scale, true);
+        o[2 * i] = f32x2_to_bf16x2(lo[0], lo[1]);
+        o[2 * i + 1] = f32x2_to_bf16x2(hi[0], hi[1]);
     }
     return uint4{o[0], o[1], o[2], o[3]};
 }
@@ -77,8 +78,8 @@ __global__ __launch_bounds__(kThreads) void k_encode(const uint16_t* __restrict_
 // out[inv_perm[t, k]] = token t's row, bf16 as it is or restored from 8 bits,
 // and row_weights[inv_perm[t, k]] = topk_w[t, k]; inv_perm null: out[t].  One
 // wave takes a token and a share of its picks and reads its row once for them,
-// kSlabs slabs of 512 columns at a time.
-template <bool CODES>
+// kSlabs slabs of 512 columns at a time.  NT: non-temporal stores.
+template <bool CODES, bool NT>
 __global__ __launch_bounds__(kThreads) void k_rows(const void* __restrict__ x, const uint8_t* __restrict__ scales,
                                                    const int32_t* __restrict__ inv_perm,
                                                    const float* __restrict__ topk_w, int64_t Mc, int K, int topk,
@@ -115,7 +116,9 @@ __global__ __launch_bounds__(kThreads) void k_rows(const void* __restrict__ x, c
 #pragma unroll
                 for (int b = 0; b < kSlabs; ++b) {
                     const int c = c0 + b * kWave * 8;
-                    if (c < K) *reinterpret_cast<uint4*>(out + row * K + c) = v[b];
+                    if (c >= K) break;
+                    if constexpr (NT) store_once16(out + row * K + c, v[b]);
+                    else *reinterpret_cast<uint4*>(out + row * K + c) = v[b];
                 }
                 if (row_weights && c0 == 0) row_weights[row] = topk_w[t * topk + k];
             }
@@ -160,7 +163,12 @@ hipError_t launch_rows(const void* x, const uint8_t* scales, const int32_t* inv_
     // a token's picks over several waves until there are 8 blocks per CU
     int64_t by = (8 * (int64_t)num_cus + bx - 1) / bx;
     by = by > topk ? topk : by;
-    auto* k = scales ? k_rows<true> : k_rows<false>;
+    // Plain stores where the rows written fit the 256 MB behind the L2s, from
+    // where the next product reads them, non-temporal ones past that.  2048
+    // columns, top-8, bf16 and restored rows, us: 4096 tokens plain 31 and 23,
+    // non-temporal 29 and 27; 16384 tokens 161 and 112, 106 and 105.
+    const bool nt = (int64_t)K * 2 * Mc * topk > (int64_t)256 << 20;
+    auto* k = scales ? (nt ? k_rows<true, true> : k_rows<true, false>) : (nt ? k_rows<false, true> : k_rows<false, false>);
     k<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, s>>>(x, scales, inv_perm, topk_w, Mc, K, topk, out, out_rows,
                                                             row_weights);
     return hipGetLastError();

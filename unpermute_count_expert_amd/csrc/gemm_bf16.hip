@@ -243,14 +243,15 @@ __device__ __forceinline__ uint32_t over_lane_rows(uint32_t v, F f) {
     return f(b[0], b[1]);
 }
 
-// four fp32 as e4m3 codes times inv
+// four fp32 times inv as e4m3 codes, and back (scale: a power of two)
 __device__ __forceinline__ uint32_t to_codes(const v4f& v, float inv) {
     const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
 }
 __device__ __forceinline__ v4f from_codes(uint32_t c, float scale) {
-    const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
-    return v4f{lo[0] * scale, lo[1] * scale, hi[0] * scale, hi[1] * scale};
+    const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, false);
+    const v2f hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, true);
+    return v4f{lo[0], lo[1], hi[0], hi[1]};
 }
 __device__ __forceinline__ uint32_t magnitude(const v4f& v) {
     uint32_t m = 0;
@@ -261,17 +262,19 @@ __device__ __forceinline__ uint32_t magnitude(const v4f& v) {
 
 // Backward through silu(g) u of four columns: d is the gradient of act, w the
 // row's weight.  act = w silu(g) u, dg and du the gradients of gate and up
-// times w; returns the sum of silu(g) u d.
+// times w; returns the sum of silu(g) u d.  silu' = s + silu (1 - s).  Twelve
+// plain operations an element beside the exponential and the reciprocal: they
+// are a third of what the epilogue costs.
 __device__ __forceinline__ float gated_bwd(const v4f& g, const v4f& u, const v4f& d, float w, v4f& act, v4f& dg,
                                            v4f& du) {
     float dot = 0.0f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const float s = sigmoid(g[q]), silu = g[q] * s, a = silu * u[q], wd = w * d[q];
-        dot = __builtin_fmaf(a, d[q], dot);
-        act[q] = w * a;
-        dg[q] = wd * u[q] * (s * (1.0f + g[q] * (1.0f - s)));
-        du[q] = wd * silu;
+        const float s = sigmoid(g[q]), silu = g[q] * s, ws = w * silu, ud = u[q] * d[q];
+        dot = __builtin_fmaf(silu, ud, dot);
+        act[q] = ws * u[q];
+        du[q] = ws * d[q];
+        dg[q] = w * __builtin_fmaf(silu, 1.0f - s, s) * ud;
     }
     return dot;
 }
@@ -284,21 +287,40 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64
                                              rows <= 0 ? 0 : max((rows - 1) * ld + last, 0), 0x00020000);
 }
 
-// What the backward epilogue reads of 16 rows by 64 columns from n0 on, a
-// lane its row (lane mod 16) and, in each half, its eight of 32 columns.
+// Two pieces of 32 columns of 16 rows, a lane its row's (lane mod 16) part of
+// each, as two pieces of 8 rows of 64 columns, and back: lanes eight apart
+// trade, so that a load or store moves whole 128-byte lines (of bf16).
+// 16384 tokens, 768 columns, bf16: stored in halves of lines 612 us, in lines
+// 590, loaded so too 573.
+template <typename V>
+__device__ __forceinline__ void trade(V& lo, V& hi) {
+#pragma unroll
+    for (int q = 0; q < (int)(sizeof(V) / 4); ++q) {
+        const uint32_t l = lo[q];
+        lo[q] = __builtin_amdgcn_update_dpp(l, hi[q], 0x128, 0xf, 0xc, false);       // row_ror:8, into lanes 8 .. 15
+        hi[q] = __builtin_amdgcn_update_dpp(hi[q], l, 0x128, 0xf, 0x3, false);       // and into lanes 0 .. 7
+    }
+}
+
+// What the backward epilogue reads of 16 rows by 64 columns from n0 on, as
+// pieces of 8 rows: rows 8 p + (lane mod 8), eight columns from traded_col().
+__device__ __forceinline__ int traded_col() {
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4;
+    return 16 * (g & 1) + 8 * (g >> 1) + (lane & 8 ? 32 : 0);
+}
 template <int KEEP>
 struct GateIn {
     v4u h[2][KEEP == kKeepBf16 ? 2 : 1];   // gate and up; codes: both in one
-    uint32_t scale;                        // lane rows: gate, gate, up, up of the two halves
+    uint32_t scale;                        // lane rows: gate, gate, up, up of the two 32 columns
     float weight;
     __device__ __forceinline__ void fetch(const Gate& gate, int N, int row0, int rows, int n0) {
         constexpr int ks = KEEP == kKeepBf16 ? 2 : 1;
-        const int lane = threadIdx.x & (kWave - 1), rl = lane & 15, g = lane >> 4, c0 = 16 * (g & 1) + 8 * (g >> 1);
-        const int w = N - n0;
+        const int lane = threadIdx.x & (kWave - 1), rl = lane & 15, g = lane >> 4;
+        const int w = N - n0, c = traded_col();
         const auto r = rows_rsrc(gate.h, ((int64_t)row0 * 2 * N + n0) * ks, rows, 2 * N * ks, (N + w) * ks);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const uint32_t at = c0 + 32 * p < w ? (uint32_t)((rl * 2 * N + c0 + 32 * p) * ks) : kNowhere;
+            const uint32_t at = c < w ? (uint32_t)(((8 * p + (lane & 7)) * 2 * N + c) * ks) : kNowhere;
             if constexpr (KEEP == kKeepBf16) {
                 h[p][0] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kNonTemporal);
                 h[p][1] = __builtin_amdgcn_raw_buffer_load_b128(r, at + N * 2, 0, kNonTemporal);
@@ -325,10 +347,10 @@ struct GateIn {
 // dot product.
 template <int KEEP>
 __device__ __forceinline__ float gated_bwd_rows(const Gate& gate, void* dh, int N, int row0, int rows, int n0,
-                                                const GateIn<KEEP>& in, const v4f (&d)[4]) {
-    const int lane = threadIdx.x & (kWave - 1), rl = lane & 15, g = lane >> 4, c0 = 16 * (g & 1) + 8 * (g >> 1);
+                                                GateIn<KEEP>& in, const v4f (&d)[4]) {
+    const int lane = threadIdx.x & (kWave - 1);
     const int w = N - n0;
-    float sc[2][2];   // [gate or up][half]
+    float sc[2][2];   // [gate or up][32 columns]
     if constexpr (KEEP == kKeepE4m3) {
         const auto a = __builtin_amdgcn_permlane32_swap(in.scale, in.scale, false, false);
 #pragma unroll
@@ -338,9 +360,10 @@ __device__ __forceinline__ float gated_bwd_rows(const Gate& gate, void* dh, int 
             sc[i][1] = e8m0_value(b[1]);
         }
     }
-    const auto rh = rows_rsrc(dh, ((int64_t)row0 * 2 * N + n0) * 2, rows, 4 * N, (N + w) * 2);
-    const auto ra = rows_rsrc(gate.act, ((int64_t)row0 * N + n0) * 2, rows, 2 * N, w * 2);
     float dot = 0.0f;
+    v4u out[3][2];   // gradients of gate and of up, act
+#pragma unroll
+    for (int x = 0; x < (KEEP == kKeepBf16 ? 2 : 1); ++x) trade(in.h[0][x], in.h[1][x]);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         v4f gx, gy, ux, uy, act[2], dg[2], du[2];
@@ -357,13 +380,24 @@ __device__ __forceinline__ float gated_bwd_rows(const Gate& gate, void* dh, int 
         }
         dot += gated_bwd(gx, ux, d[2 * p], in.weight, act[0], dg[0], du[0]);
         dot += gated_bwd(gy, uy, d[2 * p + 1], in.weight, act[1], dg[1], du[1]);
-        const int c = c0 + 32 * p;
-        const uint32_t at = c < w ? (uint32_t)((rl * 2 * N + c) * 2) : kNowhere;
-        __builtin_amdgcn_raw_buffer_store_b128(pack_pair(dg[0], dg[1]), rh, at, 0, kNonTemporal);
-        __builtin_amdgcn_raw_buffer_store_b128(pack_pair(du[0], du[1]), rh, at + N * 2, 0, kNonTemporal);
+        out[0][p] = pack_pair(dg[0], dg[1]);
+        out[1][p] = pack_pair(du[0], du[1]);
+        out[2][p] = pack_pair(act[0], act[1]);
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) trade(out[x][0], out[x][1]);
+    const auto rh = rows_rsrc(dh, ((int64_t)row0 * 2 * N + n0) * 2, rows, 4 * N, (N + w) * 2);
+    const auto ra = rows_rsrc(gate.act, ((int64_t)row0 * N + n0) * 2, rows, 2 * N, w * 2);
+    const int c = traded_col();
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int r = 8 * p + (lane & 7);
+        const uint32_t at = c < w ? (uint32_t)((r * 2 * N + c) * 2) : kNowhere;
+        __builtin_amdgcn_raw_buffer_store_b128(out[0][p], rh, at, 0, kNonTemporal);
+        __builtin_amdgcn_raw_buffer_store_b128(out[1][p], rh, at + N * 2, 0, kNonTemporal);
         if (gate.act)
-            __builtin_amdgcn_raw_buffer_store_b128(pack_pair(act[0], act[1]), ra,
-                                                   c < w ? (uint32_t)((rl * N + c) * 2) : kNowhere, 0, kNonTemporal);
+            __builtin_amdgcn_raw_buffer_store_b128(out[2][p], ra, c < w ? (uint32_t)((r * N + c) * 2) : kNowhere, 0,
+                                                   kNonTemporal);
     }
     return dot;
 }
@@ -908,7 +942,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     // row blocks ahead of their use.
     auto store_gated_bwd = [&]() __attribute__((always_inline)) {
         if (!done.mine) return;
-        constexpr int kAheadRows = 3;
+        constexpr int kAheadRows = 2;
         const int nd = (N + 63) / 64;
         GateIn<KEEP> in[MI];
         auto rows_from = [&](int i) __attribute__((always_inline)) { return done.m_end - done.m0 - 16 * i; };
@@ -966,14 +1000,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     start(c);
     bool have = false;             // a finished tile's sums are in registers
     if (grp != 0) to_multiply();   // group 1 runs one phase behind
+    // The gated products store both groups' sums in the same phase, so that
+    // one's waits for memory are the other's time to compute: group 1, which
+    // has multiplied its last step in it, before the barrier that ends it,
+    // group 0 after the one that begins it, which therefore stands at the end
+    // of its step.
+    constexpr bool PAIR = GATED || GBWD;
+    auto enter = [&]() __attribute__((always_inline)) {
+        to_read();
+        if (BT) puts();
+        sched_fence();
+    };
+    if (PAIR && grp == 0) enter();
     while (c.valid) {
         const Part t = part_of(c);
         int left = depth(c);
         bool first = true;
         do {   // an expert without rows: one step, of zeros
-            to_read();
-            if (BT) puts();
-            sched_fence();
+            if (!PAIR) enter();
             if (first) {
                 if (have) store();
                 sched_fence();
@@ -982,6 +1026,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
                 first = false;
                 have = true;
             }
+            if (PAIR && grp != 0) enter();
             v8bf fa[2][MI], fb[2][NJ];   // the step's fragments: dead between steps, where the stores need registers
             // (ACC: read whether they are used or not; else what the last step
             // left would pass for them, and the registers are taken in store())
@@ -991,10 +1036,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
             to_multiply();
             if (t.mine) multiply(fa, fb);
             left -= BK;
+            if (PAIR && grp == 0) enter();
         } while (left > 0);
         next(c);
     }
-    if (grp == 0) to_read();   // as many barriers as group 1
+    if (!PAIR && grp == 0) to_read();   // as many barriers as group 1
     if (have) store();
     wait_loads<0>();   // no load may still write this block's LDS when it ends
 }

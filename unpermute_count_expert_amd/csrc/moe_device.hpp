@@ -133,7 +133,8 @@ __device__ __forceinline__ uint32_t e8m0_of(uint32_t m) {
 // 1 / its value, exact; for 255 an infinity, with which every value of the
 // block becomes the NaN code (0 included)
 __device__ __forceinline__ float e8m0_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
-__device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b << 23 | (b == 255u ? 1u : 0u)); }
+// as the scale of a conversion, which reads the exponent (0: 2^-127)
+__device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b << 23); }
 
 // eight bf16 values (one 16-byte load) as fp32
 __device__ __forceinline__ void bf16x8_to_f32(uint4 u, float (&v)[8]) {
