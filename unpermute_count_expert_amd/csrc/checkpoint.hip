@@ -23,12 +23,20 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
     return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, false));   // lanes 2 3 0 1
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
+typedef short v2s __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float scale) {
     uint2 c;
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-    c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
-    c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, w, true);
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v2s p = {0, 0};
+        p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, v[4 * i], v[4 * i + 1], scale, false);
+        p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, v[4 * i + 2], v[4 * i + 3], scale, true);
+        w[i] = __builtin_bit_cast(uint32_t, p);
+    }
+    c.x = w[0];
+    c.y = w[1];
     return c;
 }
 
@@ -68,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void k_encode(const uint16_t* __restrict_
             for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
             const uint32_t e = e8m0_of(quad_max(m));
             if (o >= octets) break;
-            const uint2 c = encode8(v, e8m0_inverse(e));
+            const uint2 c = encode8(v, e8m0_value(e));
             *reinterpret_cast<uint2*>(q + o * 8) = c;
             if ((threadIdx.x & 3) == 0) scales[o >> 2] = (uint8_t)e;
         }

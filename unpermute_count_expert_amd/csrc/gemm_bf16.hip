@@ -223,6 +223,7 @@ __device__ __forceinline__ void unpack_pair(const v4u& v, v4f& x, v4f& y) {
 // ---- the gated products' epilogues ----------------------------------------------
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
+typedef short v2s __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
@@ -243,10 +244,12 @@ __device__ __forceinline__ uint32_t over_lane_rows(uint32_t v, F f) {
     return f(b[0], b[1]);
 }
 
-// four fp32 times inv as e4m3 codes, and back (scale: a power of two)
-__device__ __forceinline__ uint32_t to_codes(const v4f& v, float inv) {
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
+// four fp32 over a power of two as e4m3 codes, and back
+__device__ __forceinline__ uint32_t to_codes(const v4f& v, float scale) {
+    v2s c = {0, 0};
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[0], v[1], scale, false);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[2], v[3], scale, true);
+    return __builtin_bit_cast(uint32_t, c);
 }
 __device__ __forceinline__ v4f from_codes(uint32_t c, float scale) {
     const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, false);
@@ -926,8 +929,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
                 for (int half = 0; half < 2; ++half) {
                     const v4f &x = s[2 * half], &y = s[2 * half + 1];
                     const uint32_t e = e8m0_of(row_max(max(magnitude(x), magnitude(y))));
-                    const float inv = e8m0_inverse(e);
-                    const auto c = __builtin_amdgcn_permlane16_swap(to_codes(x, inv), to_codes(y, inv), false, false);
+                    const float scale32 = e8m0_value(e);
+                    const auto c = __builtin_amdgcn_permlane16_swap(to_codes(x, scale32), to_codes(y, scale32), false, false);
                     __builtin_amdgcn_raw_buffer_store_b64(v2u{c[0], c[1]}, rh, vh + half * N, 0, 0);
                     scale[half] = g == (i & 3) ? e : scale[half];
                     if ((i & 3) == 3)   // four row blocks' scales at a time: lane l row l's
@@ -1254,7 +1257,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t e = e8m0_of(max(__float_as_uint(s_red[0][0][j * 16 + rl]), __float_as_uint(s_red[1][0][j * 16 + rl])));
-                    __builtin_amdgcn_raw_buffer_store_b32(to_codes(acc[j], e8m0_inverse(e)), rh,
+                    __builtin_amdgcn_raw_buffer_store_b32(to_codes(acc[j], e8m0_value(e)), rh,
                                                           (uint32_t)(rl * 2 * N + j * N + 4 * g), 0, 0);
                     __builtin_amdgcn_raw_buffer_store_b8(
                         (uint8_t)e, rs, uw == 0 && g == 0 ? (uint32_t)(rl * (N / 16) + j * (N / 32)) : kNowhere, 0, 0);
@@ -1318,14 +1321,22 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
         const double experts = rows_hint < El ? (double)rows_hint : El, r = (double)rows_hint / experts;
         const double bytes = experts * N * C * 2 / 5.5e6;   // the weights' time
         const double units = experts * std::max(1.0, r / 16 + 0.75) * ((N + NC - 1) / NC) / (2 * cus);
-        const double few = 3.5 + std::max(1.0, units) *
-                                     (1.5 + (FWD ? 0.85 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
+        // The gated products' constants are their own fit, to 160 calls (1 to
+        // 100000 rows, 1 to 128 experts): 0.7% slower than the best of the
+        // three on average (with the others' constants 1.4%), over 20% in 2.
+        // Their epilogues weigh more in a tile, so the larger tile has to save
+        // more rounds: two fifths in the backward pass (128 experts of 768 x
+        // 2048, 256 rows each: 192 us with 128 rows, 220 with 256; 1024 rows
+        // each 612 and 540).
+        constexpr bool G = MODE == kGated || MODE == kGatedBwd;
+        const double few = 3.5 + std::max(1.0, units) * ((MODE == kGatedBwd ? 1.0 : 1.5) +
+                                     (FWD ? G ? 0.72 : 0.85 : G ? 1.02 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
         // rounds of tiles; 128 rows unless 256 save more than a fifth of them
         const double rounds1 = experts * std::max(1.0, r / 128 + 0.5) * ntn / cus;
         const double rounds2 = experts * std::max(1.0, r / 256 + 0.5) * ntn / cus;
-        const bool low = 4 * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
+        const bool low = (MODE == kGatedBwd ? 3 : 4) * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
         const double walk = 6.5 + std::max(1.0, low ? rounds1 : rounds2) *
-                                      (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
+                                      ((G && low ? 5.0 : 1.7) + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
         if (std::max(few, bytes) <= std::max(walk, bytes + 1))
             k_few<MODE, KEEP><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
                                                         static_cast<uint16_t*>(out), gate);

@@ -130,10 +130,8 @@ __device__ __forceinline__ uint32_t e8m0_of(uint32_t m) {
     const int e = (int)((m + 0x1fffffu) >> 23) - 8;
     return m >= 0x7f800000u ? 255u : (uint32_t)max(e, 10);
 }
-// 1 / its value, exact; for 255 an infinity, with which every value of the
-// block becomes the NaN code (0 included)
-__device__ __forceinline__ float e8m0_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
-// as the scale of a conversion, which reads the exponent (0: 2^-127)
+// Its value as the scale of a conversion, which reads the exponent bits alone
+// (b = 0 is 2^-127 there, 255 makes a value or code NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b << 23); }
 
 // eight bf16 values (one 16-byte load) as fp32
