@@ -909,7 +909,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         const int rl = lane & 15, w = N - done.n0;
         const uint32_t va = c0 < w ? (uint32_t)((rl * N + c0) * 2) : kNowhere;
         const uint32_t vh = c0 < w ? (uint32_t)((rl * 2 * N + c0) * ks) : kNowhere;
-        uint32_t scale[2] = {0, 0};   // of gate and of up, a row block's in each lane row
+        uint32_t scale = 0;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const v4f (&s)[NJ] = acc[i];
@@ -923,20 +923,28 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
                 __builtin_amdgcn_raw_buffer_store_b128(pack_pair(s[2], s[3]), rh, vh + N * 2, 0, 0);
             }
             if constexpr (KEEP == kKeepE4m3) {
-                const auto rs = rows_rsrc(gate.h_s, (int64_t)(row0 - 16 * (i & 3)) * (N / 16) + done.n0 / 32,
-                                          min(rows + 16 * (i & 3), 64), N / 16, N / 32 + 1);
+                // both largest magnitudes in one reduction: lane rows 0 and 1
+                // end with gate's, 2 and 3 with up's
+                const auto m = __builtin_amdgcn_permlane32_swap(max(magnitude(s[0]), magnitude(s[1])),
+                                                                max(magnitude(s[2]), magnitude(s[3])), false, false);
+                const uint32_t m2 = max(m[0], m[1]);
+                const auto m4 = __builtin_amdgcn_permlane16_swap(m2, m2, false, false);
+                const uint32_t e = e8m0_of(max(m4[0], m4[1]));
+                const auto both = __builtin_amdgcn_permlane32_swap(e, e, false, false);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const v4f &x = s[2 * half], &y = s[2 * half + 1];
-                    const uint32_t e = e8m0_of(row_max(max(magnitude(x), magnitude(y))));
-                    const float scale32 = e8m0_value(e);
-                    const auto c = __builtin_amdgcn_permlane16_swap(to_codes(x, scale32), to_codes(y, scale32), false, false);
+                    const float sc = e8m0_value(both[half]);
+                    const auto c = __builtin_amdgcn_permlane16_swap(to_codes(s[2 * half], sc), to_codes(s[2 * half + 1], sc),
+                                                                    false, false);
                     __builtin_amdgcn_raw_buffer_store_b64(v2u{c[0], c[1]}, rh, vh + half * N, 0, 0);
-                    scale[half] = g == (i & 3) ? e : scale[half];
-                    if ((i & 3) == 3)   // four row blocks' scales at a time: lane l row l's
-                        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)scale[half], rs,
-                                                             (uint32_t)(lane * (N / 16) + half * (N / 32)), 0, 0);
                 }
+                scale = (g & 1) == (i & 1) ? e : scale;
+                if (i & 1)   // two row blocks' scales at a time, gate's and up's
+                    __builtin_amdgcn_raw_buffer_store_b8(
+                        (uint8_t)scale,
+                        rows_rsrc(gate.h_s, (int64_t)(row0 - 16) * (N / 16) + done.n0 / 32, min(rows + 16, 32), N / 16,
+                                  N / 32 + 1),
+                        (uint32_t)((16 * (g & 1) + rl) * (N / 16) + (g >> 1) * (N / 32)), 0, 0);
             }
             sched_fence();
         }
