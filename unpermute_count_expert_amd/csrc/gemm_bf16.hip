@@ -5,6 +5,12 @@
 //   dgrad    dx[r,k]  = sum_n dy[r,n] w[e,n,k]          (contraction: n)
 //   wgrad    dw[e,n,k] (+)= sum_{r of e} dy[r,n] a[r,k] (contraction: e's rows)
 //
+// and the same products with the experts' activation in their epilogues:
+//
+//   gated      h = a w13^T (gate and up columns), act = silu(gate) up
+//   gated bwd  d = dy w2, and from gate and up as they were kept dh, act and
+//              the router weight's share of the gradient
+//
 // fp32 sums, one rounding to bf16.  Two kernels:
 //
 // k_tiles, for experts of more than a few rows.
@@ -64,6 +70,31 @@
 //    are then read by tiles that run together (n-tiles fastest: forward 1-5%
 //    and weight gradient 5% slower), and the operand stream runs ahead across
 //    tile boundaries.
+//
+// The gated modes of k_tiles (MODE kGated, kGatedBwd).
+//  * Forward, a tile is 128 gate columns and the same up columns: half of each
+//    weight granule's rows are gate rows, half up rows, so a lane ends with
+//    both and h needs no trip through memory.  It is kept for the backward
+//    pass as it is (KEEP): not at all, in bf16, or as e4m3 codes with a scale
+//    for 32 columns, which lie in one wave's four lane rows.
+//  * 16384 tokens, top-8, 128 experts, 768 x 2048, us: h not kept 726-748, bf16
+//    781-803, 8 bits 791-810, against 750 for the product and 95 for SiLU-mul.
+//    Backward from bf16 551, from 8 bits 540, against 395 for the product and
+//    163 for SiLU-mul's gradient, which leave out act and the dot products.
+//  * The backward epilogue reads 2 or 4 and writes 6 bytes an element, half of
+//    the kernel's bytes, and costs 165 us: 70 for its operations (12 plain ones
+//    an element, an exponential and a reciprocal), the rest for memory.  With
+//    its operand reads (1.7-1.9 GB of 1.0 past the L2s) the kernel moves 2.3-2.5
+//    GB, 4.2-4.6 TB/s.  What counted: both groups' stores in one phase, whole
+//    lines (trade()), h read two row blocks ahead (three spill).  8 bits
+//    forward: one reduction for both scales (814 -> 791).
+//  * Not kept: blocks starting a part of a tile apart (level to 3% slower), two
+//    independent blocks of four waves a CU instead of two groups (product 450
+//    us, backward 580), a finished 128-row tile's row blocks stored one by one
+//    under the next tile's steps (1280: a wait for what was read drains the
+//    operand stream), h's first row blocks read before the last multiplies
+//    (spills), forward waves of 64 gate and 64 up columns, whole lines of act
+//    (level), n-tiles fastest (level).
 //
 // k_few, for a few rows per expert (decoding), where the weights' bytes are
 // the time and 256-column tiles would leave most CUs idle: 16 rows by 32 (64
@@ -1214,7 +1245,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
                 for (int w = 0; w < 3; ++w)
                     acc[j] += *reinterpret_cast<const v4f*>(&s_red[uw][w][(j * kWave + lane) * 4]);
             const int w = N - x.n0;   // columns from n0 on
-            if constexpr (GATED) {
+            if constexpr (GATED) {   // a lane: four columns of gate (block 0) and of up (block 1)
                 const int rl = lane & 15;
                 const uint32_t c = (uint32_t)(4 * g);
                 const v4f a = gated(acc[0], acc[1]);
@@ -1245,14 +1276,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
                         __float_as_uint(dot), rows_rsrc(gate.dots, ((int64_t)x.m0 * nd + x.n0 / 64) * 4, x.rows, 4 * nd, 4),
                         lane < 16 ? (uint32_t)(lane * 4 * nd) : kNowhere, 0, 0);
             } else {
-            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                out + (int64_t)x.m0 * N + x.n0, 0, x.rows > 0 ? ((x.rows - 1) * N + w) * 2 : 0, 0x00020000);
+                const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                    out + (int64_t)x.m0 * N + x.n0, 0, x.rows > 0 ? ((x.rows - 1) * N + w) * 2 : 0, 0x00020000);
 #pragma unroll
-            for (int p = 0; p < NJ / 2; ++p) {
-                const int c = 32 * p + 16 * (g & 1) + 8 * (g >> 1);
-                const uint32_t v = c < w ? (uint32_t)(((lane & 15) * N + c) * 2) : kNowhere;
-                __builtin_amdgcn_raw_buffer_store_b128(pack_pair(acc[2 * p], acc[2 * p + 1]), r, v, 0, 0);
-            }
+                for (int p = 0; p < NJ / 2; ++p) {
+                    const int c = 32 * p + 16 * (g & 1) + 8 * (g >> 1);
+                    const uint32_t v = c < w ? (uint32_t)(((lane & 15) * N + c) * 2) : kNowhere;
+                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair(acc[2 * p], acc[2 * p + 1]), r, v, 0, 0);
+                }
             }
         }
         if constexpr (GATED && KEEP == kKeepE4m3) {
@@ -1328,23 +1359,23 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
         const int C = FWD ? k_in : n_out;
         const double experts = rows_hint < El ? (double)rows_hint : El, r = (double)rows_hint / experts;
         const double bytes = experts * N * C * 2 / 5.5e6;   // the weights' time
-        const double units = experts * std::max(1.0, r / 16 + 0.75) * ((N + NC - 1) / NC) / (2 * cus);
-        // The gated products' constants are their own fit, to 160 calls (1 to
-        // 100000 rows, 1 to 128 experts): 0.7% slower than the best of the
-        // three on average (with the others' constants 1.4%), over 20% in 2.
-        // Their epilogues weigh more in a tile, so the larger tile has to save
-        // more rounds: two fifths in the backward pass (128 experts of 768 x
-        // 2048, 256 rows each: 192 us with 128 rows, 220 with 256; 1024 rows
-        // each 612 and 540).
-        constexpr bool G = MODE == kGated || MODE == kGatedBwd;
-        const double few = 3.5 + std::max(1.0, units) * ((MODE == kGatedBwd ? 1.0 : 1.5) +
-                                     (FWD ? G ? 0.72 : 0.85 : G ? 1.02 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
+        // The backward gated product has constants of its own fit, to 800 calls
+        // (1 to 100000 rows, 1 to 128 experts): 1.4% slower than the best of
+        // the three on average, over 20% in 22 and 49% at worst (with the
+        // others' constants 2.1%, 37 and 87%; forward those give 1.1%, 18 and
+        // 43%).  Its epilogue weighs more in a tile, so the larger tile has to
+        // save two fifths of the rounds: 128 experts of 768 x 2048, 256 rows
+        // each, 195 us with 128 rows and 220 with 256; 1024 rows each, 597 and 545.
+        constexpr bool BWD = MODE == kGatedBwd;
+        const double units = experts * std::max(1.0, r / 16 + (BWD ? 1.0 : 0.75)) * ((N + NC - 1) / NC) / (2 * cus);
+        const double few = 3.5 + std::max(1.0, units) * ((BWD ? 0.7 : 1.5) +
+                                     (FWD ? 0.85 : BWD ? 1.08 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
         // rounds of tiles; 128 rows unless 256 save more than a fifth of them
         const double rounds1 = experts * std::max(1.0, r / 128 + 0.5) * ntn / cus;
         const double rounds2 = experts * std::max(1.0, r / 256 + 0.5) * ntn / cus;
-        const bool low = (MODE == kGatedBwd ? 3 : 4) * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
-        const double walk = 6.5 + std::max(1.0, low ? rounds1 : rounds2) *
-                                      ((G && low ? 5.0 : 1.7) + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
+        const bool low = (BWD ? 3 : 4) * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
+        const double walk = (BWD ? 8.0 : 6.5) + std::max(1.0, low ? rounds1 : rounds2) *
+                                      (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
         if (std::max(few, bytes) <= std::max(walk, bytes + 1))
             k_few<MODE, KEEP><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
                                                         static_cast<uint16_t*>(out), gate);
