@@ -5,7 +5,8 @@ with topk weight and reduce, chunked over tokens.
 The compute lives in libmoe_hip.so (C ABI in include/moe.h); this package is
 its ctypes binding plus small device-resident layer wrappers: MoeLayer (fp8
 weights, forward) and MoeTrainLayer (bf16 weights, forward and backward, with
-the gradients' global norm and clipping).
+the gradients' global norm and clipping; with a checkpoint on fused kernels
+and less memory, in bf16 or 8 bits).
 """
 from ._lib import (MOE_ACT_IDENTITY, MOE_ACT_SILU_MUL, MoeError, MoeProblem, load,  # noqa: F401
                    moe_act_quant, moe_count, moe_forward_chunked, moe_forward_workspace_size, moe_forward_workspace_slices,
