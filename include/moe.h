@@ -495,7 +495,8 @@ int moe_grouped_gemm_bf16_silu_mul(const uint16_t* a, const uint16_t* w13, const
  * router's weights, act is what the gradient by w2 needs beside dy, and
  * moe_topk_weights_bwd makes the router weights' gradient of dots: the down
  * product's output is not needed.  With dy already weighted, p is 1 and the
- * dots are not the weights' gradient.  dy [cap_rows,k_out], w2 [El,k_out,n],
+ * dots are not the weights' gradient.  Sigmoid and overflow of d * u as in
+ * moe_silu_mul_bwd.  dy [cap_rows,k_out], w2 [El,k_out,n],
  * h and dh [cap_rows,2n], act [cap_rows,n], row_weights [cap_rows], dots
  * [cap_rows, (n + 63) / 64]; n as above.  dh may be h itself where that is
  * bf16 (in place); apart from that no output overlaps an input or another
