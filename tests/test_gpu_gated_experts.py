@@ -532,6 +532,19 @@ def test_gated_long_walks(cs, n, k):
     gated_on_gpu(cs, n, k, off, cap, (1, sum(cs), 1 << 24), len(cs))
 
 
+@pytest.mark.parametrize("E,n,k,rows", [(128, 768, 2048, (1, 16, 64, 160, 300, 1024)), (60, 416, 264, (1, 20, 100, 700, 5000)),
+                                        (513, 64, 264, (1, 20, 160, 2000)), (512, 32, 136, (1, 40, 3000))])
+def test_gated_every_kernel(E, n, k, rows):
+    """Experts and row counts given that pick each kernel in turn (a few rows; 64-, 128- and 256-row tiles, the
+    forward ones with staggered and with common starts of the contraction; no 64-row tiles past 512 experts)."""
+    announce("gated every kernel", E, n, k)
+    g = torch.Generator().manual_seed(n + k)
+    cs = torch.randint(0, 30, (E,), generator=g).tolist()
+    cs[3], cs[E // 2], cs[E - 1] = 0, 150, 290
+    off, cap = segments(cs, 16)
+    gated_on_gpu(cs, n, k, off, cap, [1] + [r * E for r in rows], n + k, ("bf16", "e4m3"))
+
+
 @pytest.mark.parametrize("n,k", [(32768, 8), (32, 65536), (96, 30000)])
 def test_gated_widest(n, k):
     announce("gated widest", n, k)

@@ -95,6 +95,9 @@
 //    operand stream), h's first row blocks read before the last multiplies
 //    (spills), forward waves of 64 gate and 64 up columns, whole lines of act
 //    (level), n-tiles fastest (level).
+//  * For a few hundred rows, where 256-column tiles are too few for the CUs,
+//    tiles of 64 x 128 (SMALL), three blocks a CU.  Four blocks with a ring of
+//    4 granules, two with 9, and 128 rows a tile: level to 5% slower.
 //
 // k_few, for a few rows per expert (decoding), where the weights' bytes are
 // the time and 256-column tiles would leave most CUs idle: 16 rows by 32 (64
@@ -168,8 +171,8 @@ __device__ __forceinline__ void segments(const int32_t* __restrict__ offsets, co
 // Exclusive prefix over the experts of nt (two consecutive experts a thread)
 // into pre[0 .. El), and the total, both capped at `most`: disjoint segments
 // never reach the cap, and overlapping ones (offsets out of order) cannot
-// push a sum past it.  wsum: LDS scratch of kWaves values.  All 512 threads
-// call it; it ends with a barrier.
+// push a sum past it.  wsum: LDS scratch of kWaves values.  All threads of a
+// block call it; it ends with a barrier.
 __device__ __forceinline__ int expert_prefix(const int (&nt)[2], int El, int64_t most, int* pre, int64_t* wsum) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t sum = (int64_t)nt[0] + nt[1];
@@ -177,7 +180,7 @@ __device__ __forceinline__ int expert_prefix(const int (&nt)[2], int El, int64_t
     if (lane == kWave - 1) wsum[wave] = incl;
     __syncthreads();
     int64_t run = incl - sum, total = 0;
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < (int)(blockDim.x / kWave); ++w) {
         const int64_t v = wsum[w];
         if (w < wave) run += v;
         total += v;
@@ -451,6 +454,11 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 constexpr int kGran = 8192;   // a granule
 constexpr int kRing = 19;     // granules in the ring
 constexpr int kTab = 2048;    // ints beside it: together the CU's 160 KB
+constexpr int kSmallBlocks = 3;         // SMALL: blocks on a CU,
+constexpr int kSmallThreads = 256;
+constexpr int kSmallRing = 6;           // each with two steps' granules
+constexpr int kSmallTab = 1024;         // and 52 KB in all
+constexpr int kSmallExperts = 2 * kSmallThreads;   // at most
 
 // One block's tiles t, t + nslots, ... ; all fields are wave-uniform.
 struct Cursor {
@@ -475,19 +483,28 @@ struct Cursor {
 // the loads that a wave has issued after the one needed; they are exact,
 // because past the last tile the stream goes on with loads of zero bytes.
 // F32: fp32 outputs; ACC: added to what is there.
-template <int MODE, int NA, bool F32, bool ACC, bool TURN, int KEEP>   // TURN: forward only; KEEP: gated only
-__global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
-                                                       const int32_t* __restrict__ offsets,
-                                                       const int32_t* __restrict__ counts, int El, int64_t cap_rows,
-                                                       int n_out, int k_in, void* out, Gate gate) {
+//
+// SMALL (gated modes, one granule of rows): a tile of 64 x 128 for one group of
+// four waves, 32 x 64 each, in blocks of their own, three on a CU.  A step is
+// three granules; its block reads them into registers, refills them with the
+// step after the next and multiplies; what the waits and barriers of one
+// block cost, the others fill.
+template <int MODE, int NA, bool F32, bool ACC, bool TURN, int KEEP, bool SMALL>   // TURN: forward only; KEEP: gated only
+__global__ __launch_bounds__(SMALL ? kSmallThreads : kThreads, SMALL ? kSmallBlocks : 1) void k_tiles(
+    const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ counts, int El, int64_t cap_rows, int n_out, int k_in, void* out, Gate gate) {
     constexpr bool GATED = MODE == kGated, FWD = MODE == kFwd || GATED, GBWD = MODE == kGatedBwd;
     constexpr bool DG = MODE == kDgrad || GBWD;
-    constexpr int TN = GATED ? BN / 2 : BN;   // columns of a tile; GATED: of gate and of up
-    constexpr int MI = 4 * NA, BM = 128 * NA, NJ = 4;
+    static_assert(!SMALL || (NA == 1 && (GATED || GBWD)), "one granule of rows");
+    constexpr int NB = SMALL ? 2 : BN / 64;           // granules of the weight-side operand
+    constexpr int TN = GATED ? 32 * NB : 64 * NB;     // columns of a tile; GATED: of gate and of up
+    constexpr int MI = SMALL ? 2 : 4 * NA, BM = SMALL ? 64 : 128 * NA, NJ = 4;
+    constexpr int kWaves = SMALL ? kSmallThreads / kWave : moe::kWaves;
+    constexpr int kRing = SMALL ? kSmallRing : moe::kRing, kTab = SMALL ? kSmallTab : moe::kTab;
     constexpr bool AT = MODE == kWgrad, BT = !FWD;   // column layout
-    constexpr int P = 2 * NA + 4, R = kRing % P;
+    constexpr int P = SMALL ? NA + NB : 2 * NA + NB, R = kRing % P;
     constexpr int kAhead = (kRing - NA - 4) / P;   // the step that the first even phase goes on loading
-    static_assert(R <= 4 && (kRing - NA - 4) % P == R + NA, "the phases' shares of a step");
+    static_assert(SMALL ? R == 0 : R <= 4 && (kRing - NA - 4) % P == R + NA, "the phases' shares of a step");
     // loads (two a granule and wave) issued after the last one needed: group
     // 0 before even and odd phases, group 1 before even ones (its granules
     // are all needed there)
@@ -499,7 +516,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int grp = wave >> 2, wn = wave & 3;
+    const int grp = SMALL ? 0 : wave >> 2, wn = wave & 3;
     const int N = FWD ? n_out : k_in;   // output columns
 
     // The experts in the order their tiles are walked, and, where they fit,
@@ -702,7 +719,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     };
     d_tile();
     auto put = [&](int p) __attribute__((always_inline)) {   // granule p of the step
-        const bool isA = p < NA || p >= NA + 4;
+        const bool isA = p < NA || p >= NA + NB;
         const int g = p < NA ? p : isA ? p - 4 : p - NA;
         const bool T = isA ? AT : BT;
         const int ld = isA ? ldA : ldB, go = g * (isA ? gA : gB);
@@ -761,7 +778,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
         else odd_puts();
     };
     // the ring but for what the first even phase loads
-    if (grp == 0) {
+    if constexpr (SMALL) {
+#pragma unroll
+        for (int q = 0; q < kRing; ++q) {
+            put(q % P);
+            if (q % P == P - 1) advance();
+        }
+    } else if (grp == 0) {
 #pragma unroll
         for (int q = 0; q < kRing - NA - 4; ++q) {
             if (q % P < R || q % P >= R + NA) put(q % P);
@@ -788,16 +811,21 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     };
     v4f acc[MI][NJ];
     auto load = [&](v8bf (&fa)[2][MI], v8bf (&fb)[2][NJ]) __attribute__((always_inline)) {
-        const uint32_t bB = granule(NA + wn) + rB;
+        const uint32_t bB = granule(NA + (SMALL ? wn & 1 : wn)) + rB;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) fb[ks][j] = frag(BT, bB, j, ks);
+            if constexpr (SMALL) {   // half of the rows' granule
 #pragma unroll
-            for (int g = 0; g < NA; ++g) {
-                const uint32_t bA = granule((grp ? NA + 4 : 0) + g) + rA;
+                for (int i = 0; i < MI; ++i) fa[ks][i] = frag(AT, granule(0) + rA, MI * (wn >> 1) + i, ks);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) fa[ks][4 * g + i] = frag(AT, bA, i, ks);
+                for (int g = 0; g < NA; ++g) {
+                    const uint32_t bA = granule((grp ? NA + 4 : 0) + g) + rA;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fa[ks][4 * g + i] = frag(AT, bA, i, ks);
+                }
             }
         }
     };
@@ -817,9 +845,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     } done = {0, 0, 0, 0, false};
     auto part_of = [&](const Cursor& c) __attribute__((always_inline)) {
         Part t;
-        t.m0 = m_first(c) + grp * 64 * NA;
+        t.m0 = m_first(c) + (SMALL ? (wn >> 1) * 16 * MI : grp * 64 * NA);
         t.m_end = MODE == kWgrad ? n_out : c.hi;
-        t.n0 = c.tn * TN + wn * (TN / 4);
+        t.n0 = c.tn * TN + (SMALL ? (wn & 1) * (TN / 2) : wn * (TN / 4));
         t.e = c.x;
         t.mine = t.m0 < t.m_end && t.n0 < N;
         return t;
@@ -1000,11 +1028,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
             const float dot = row_sum(gated_bwd_rows<KEEP>(gate, out, N, done.m0 + 16 * i, min(rows_from(i), 16), done.n0,
                                                            in[i], acc[i]));
             dots = g == (i & 3) ? dot : dots;
-            if (gate.dots && (i & 3) == 3)
+            constexpr int kDotRows = MI < 4 ? MI : 4;   // row blocks a store
+            if (gate.dots && i % kDotRows == kDotRows - 1)
                 __builtin_amdgcn_raw_buffer_store_b32(
                     __float_as_uint(dots),
-                    rows_rsrc(gate.dots, ((int64_t)(done.m0 + 16 * (i - 3)) * nd + done.n0 / 64) * 4,
-                              min(rows_from(i - 3), 64), 4 * nd, 4),
+                    rows_rsrc(gate.dots, ((int64_t)(done.m0 + 16 * (i + 1 - kDotRows)) * nd + done.n0 / 64) * 4,
+                              min(rows_from(i + 1 - kDotRows), 16 * kDotRows), 4 * nd, 4),
                     (uint32_t)(lane * 4 * nd), 0, 0);
             sched_fence();
         }
@@ -1041,6 +1070,44 @@ __global__ __launch_bounds__(kThreads, 1) void k_tiles(const uint16_t* __restric
     Cursor c;
     start(c);
     bool have = false;             // a finished tile's sums are in registers
+    if constexpr (SMALL) {
+        while (c.valid) {
+            const Part t = part_of(c);
+            int left = depth(c);
+            bool first = true;
+            do {
+                if (first) {
+                    if (have) store();
+                    sched_fence();
+                    done = t;
+                    begin();
+                    first = false;
+                    have = true;
+                }
+                sched_fence();
+                wait_loads<2 * (kRing - P)>();   // this step's granules; the next one's may be in flight
+                barrier();
+                sched_fence();
+                v8bf fa[2][MI], fb[2][NJ];
+                load(fa, fb);
+                c_q = c_q + P >= kRing ? c_q + P - kRing : c_q + P;
+                sched_fence();
+                wait_loads<63>();   // LDS reads only
+                barrier();          // every wave has read them: they may be overwritten
+                sched_fence();
+#pragma unroll
+                for (int p = 0; p < P; ++p) put(p);
+                advance();
+                sched_fence();
+                if (t.mine) multiply(fa, fb);
+                left -= BK;
+            } while (left > 0);
+            next(c);
+        }
+        if (have) store();
+        wait_loads<0>();   // no load may still write this block's LDS when it ends
+        return;
+    }
     if (grp != 0) to_multiply();   // group 1 runs one phase behind
     // The gated products store both groups' sums in the same phase, so that
     // one's waits for memory are the other's time to compute: group 1, which
@@ -1352,36 +1419,54 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
     if constexpr (MODE == kWgrad) {
         const double rounds1 = std::ceil((double)El * ((n_out + 127) / 128) * ntn / cus);
         const double rounds2 = std::ceil((double)El * ((n_out + 255) / 256) * ntn / cus);
-        if (3 * rounds1 <= 5 * rounds2) tiles(k_tiles<MODE, 1, F32, ACC, false, KEEP>);
-        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP>);
+        if (3 * rounds1 <= 5 * rounds2) tiles(k_tiles<MODE, 1, F32, ACC, false, KEEP, false>);
+        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP, false>);
     } else {
         constexpr int NC = FWD ? 32 : 64, KS = FWD ? 64 : 32;   // k_few's columns and step
         const int C = FWD ? k_in : n_out;
         const double experts = rows_hint < El ? (double)rows_hint : El, r = (double)rows_hint / experts;
         const double bytes = experts * N * C * 2 / 5.5e6;   // the weights' time
-        // The backward gated product has constants of its own fit, to 800 calls
-        // (1 to 100000 rows, 1 to 128 experts): 1.4% slower than the best of
-        // the three on average, over 20% in 22 and 49% at worst (with the
-        // others' constants 2.1%, 37 and 87%; forward those give 1.1%, 18 and
-        // 43%).  Its epilogue weighs more in a tile, so the larger tile has to
-        // save two fifths of the rounds: 128 experts of 768 x 2048, 256 rows
-        // each, 195 us with 128 rows and 220 with 256; 1024 rows each, 597 and 545.
-        constexpr bool BWD = MODE == kGatedBwd;
-        const double units = experts * std::max(1.0, r / 16 + (BWD ? 1.0 : 0.75)) * ((N + NC - 1) / NC) / (2 * cus);
-        const double few = 3.5 + std::max(1.0, units) * ((BWD ? 0.7 : 1.5) +
-                                     (FWD ? 0.85 : BWD ? 1.08 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
-        // rounds of tiles; 128 rows unless 256 save more than a fifth of them
+        // The gated products have constants of their own, fitted to 800 calls
+        // each (1 to 100000 rows, 1 to 128 experts), and a fourth choice.
+        constexpr bool GF = MODE == kGated, GB = MODE == kGatedBwd, G = GF || GB;
+        const double units = experts * std::max(1.0, r / 16 + (G ? 1.0 : 0.75)) * ((N + NC - 1) / NC) / (2 * cus);
+        const double few = 3.5 + std::max(1.0, units) * ((GF ? 2.5 : GB ? 0.7 : 1.5) +
+                                     (GF ? 1.15 : GB ? 1.08 : FWD ? 0.85 : 1.2) * ((C + 4 * KS - 1) / (4 * KS)));
+        // rounds of tiles; 128 rows unless 256 save more than a fifth of them,
+        // in the gated backward pass, whose epilogue weighs more, two fifths
+        // (128 experts of 768 x 2048, 256 rows each, 195 us with 128 rows and
+        // 220 with 256; 1024 rows each, 597 and 545)
         const double rounds1 = experts * std::max(1.0, r / 128 + 0.5) * ntn / cus;
         const double rounds2 = experts * std::max(1.0, r / 256 + 0.5) * ntn / cus;
-        const bool low = (BWD ? 3 : 4) * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
-        const double walk = (BWD ? 8.0 : 6.5) + std::max(1.0, low ? rounds1 : rounds2) *
+        const bool low = (GB ? 3 : 4) * std::ceil(rounds1) <= 5 * std::ceil(rounds2);
+        const double walk = (GB ? 8.0 : 6.5) + std::max(1.0, low ? rounds1 : rounds2) *
                                       (1.7 + (low ? 0.8 : 1.1) * ((C + BK - 1) / BK));
+        if constexpr (G) {
+            // Small tiles: work for every CU where the others leave some
+            // idle, and more blocks to keep short walks' loads in flight; but
+            // an expert's weights are read again for every 64 rows.  Over 400
+            // shapes the choice among the four is 2% slower than the best on
+            // average, over 20% in 1.6% of them and 50% at worst.
+            // 130 tokens over 64 experts of 672 x 2176, both ways, us: 114, with
+            // small tiles 90; 8 experts, 309 rows each, 552 x 1408: 64 and 43;
+            // 128 of 768 x 2048, forward, 64 rows each: 152, all small 175.
+            const double mtiles = std::max(1.0, r / 64 + (GB ? 1.0 : 0.5));
+            const double rounds0 = experts * mtiles * ((N + 127) / 128) / (kSmallBlocks * cus);
+            const double small = std::max(
+                3.0 + std::max(1.0, rounds0) * (GB ? 1.0 + 0.7 * ((C + BK - 1) / BK) : 3.0 + 0.8 * ((C + BK - 1) / BK)),
+                GB ? bytes * (0.9 + 0.06 * mtiles) : bytes * (0.95 + 0.06 * mtiles) - 2);
+            if (El <= kSmallExperts && small < std::min(std::max(few, bytes), std::max(walk, bytes + 1))) {
+                k_tiles<MODE, 1, F32, ACC, FWD, KEEP, true><<<kSmallBlocks * grid, kSmallThreads, 0, s>>>(
+                    a, b, offsets, counts, El, cap_rows, n_out, k_in, out, gate);
+                return hipGetLastError();
+            }
+        }
         if (std::max(few, bytes) <= std::max(walk, bytes + 1))
             k_few<MODE, KEEP><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
                                                         static_cast<uint16_t*>(out), gate);
-        else if (low) tiles(k_tiles<MODE, 1, F32, ACC, FWD, KEEP>);
-        else if (FWD && rows_hint < (int64_t)208 * El) tiles(k_tiles<MODE, 2, F32, ACC, FWD, KEEP>);
-        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP>);
+        else if (low) tiles(k_tiles<MODE, 1, F32, ACC, FWD, KEEP, false>);
+        else if (FWD && rows_hint < (int64_t)208 * El) tiles(k_tiles<MODE, 2, F32, ACC, FWD, KEEP, false>);
+        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP, false>);
     }
     return hipGetLastError();
 }
