@@ -171,8 +171,9 @@ __device__ __forceinline__ void segments(const int32_t* __restrict__ offsets, co
 // Exclusive prefix over the experts of nt (two consecutive experts a thread)
 // into pre[0 .. El), and the total, both capped at `most`: disjoint segments
 // never reach the cap, and overlapping ones (offsets out of order) cannot
-// push a sum past it.  wsum: LDS scratch of kWaves values.  All threads of a
-// block call it; it ends with a barrier.
+// push a sum past it.  wsum: LDS scratch of a value for each of the block's
+// WAVES waves.  All its threads call it; it ends with a barrier.
+template <int WAVES = kWaves>
 __device__ __forceinline__ int expert_prefix(const int (&nt)[2], int El, int64_t most, int* pre, int64_t* wsum) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t sum = (int64_t)nt[0] + nt[1];
@@ -180,7 +181,7 @@ __device__ __forceinline__ int expert_prefix(const int (&nt)[2], int El, int64_t
     if (lane == kWave - 1) wsum[wave] = incl;
     __syncthreads();
     int64_t run = incl - sum, total = 0;
-    for (int w = 0; w < (int)(blockDim.x / kWave); ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         const int64_t v = wsum[w];
         if (w < wave) run += v;
         total += v;
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(SMALL ? kSmallThreads : kThreads, SMALL ? kSmallBlo
                 s_hi[e] = hi[j];
             }
         }
-        mtiles = expert_prefix(nt, El, cap_rows / BM + El, s_at, reinterpret_cast<int64_t*>(smem));
+        mtiles = expert_prefix<kWaves>(nt, El, cap_rows / BM + El, s_at, reinterpret_cast<int64_t*>(smem));
     }
 
     // Which tiles are this block's: those of an XCD lie side by side, so that
