@@ -445,8 +445,12 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
  * scale is the least power of two that brings the block's largest magnitude to
  * 448 or below, but at least 2^-117; codes are rounded to nearest even, so a
  * value is off by at most 2^-4 of itself, or 2^-10 of the scale if that is
- * more.  A block that holds an infinity or a NaN has b = 255 and is NaN
- * throughout.  What is restored is exact in bf16. */
+ * more (the smaller ones come back 0), and what is restored is exact in bf16.
+ * Rounding passes the range as rounding to bf16 does: magnitudes from
+ * 248 * 2^120 (3.3e38; bf16's eight largest finite values 0x7f78..0x7f7f) up
+ * to the largest fp32 value get the code of 2^128 and come back as infinities
+ * of their sign, alone in their block.  A block that holds an infinity or a
+ * NaN has b = 255 and is NaN throughout. */
 
 /* x [rows,width] bf16 -> codes q [rows,width], scales [rows,width/32].
  * width: positive multiple of 32 up to 65536. */

@@ -1,0 +1,69 @@
+"""The gated experts' operators at the border of their ranges, on each of their
+kernels and side by side, on the GPU against plain 64-bit implementations.
+Tolerances: as derived in test_gpu_gated_experts.py."""
+import pytest
+import torch
+
+import unpermute_count_expert_amd as moe
+from tests.gpu_helpers import announce
+from tests.test_gpu_bf16_experts import BF, DEV, F64, gen, segments, sentinel, valid_mask
+from tests.test_gpu_gated_experts import check_codes, decode, encode, rows_untouched, run_checkpoint, run_fwd
+
+BORDER = 248 * 2.0 ** 120   # halfway between the last code that is finite at the largest scale and 2^128
+
+
+# ---- 8 bits at the end of the range -----------------------------------------------------
+@pytest.mark.parametrize("beside", [0, 1, 31])
+def test_checkpoint_bound_for_every_finite_bf16(beside):
+    """Every finite bf16 value, alone in its block, next to another one or among 31 others, comes back within the
+    documented bound; from the border on as an infinity of its sign, which leaves the rest of its block finite."""
+    announce("checkpoint bound", beside)
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF)
+    v = bits[torch.isfinite(bits.float())]
+    x = torch.zeros(len(v), 32, dtype=BF)
+    x[:, 9] = v
+    g = gen(beside)
+    for j in range(beside):
+        x[:, j if j < 9 else j + 1] = v[torch.randperm(len(v), generator=g)]
+    q, s = run_checkpoint(x)
+    out = sentinel(x.shape)
+    moe.moe_checkpoint_restore(q, s, out)
+    out, x64 = out.cpu().double(), x.double()
+    past = x64.abs() >= BORDER
+    assert past.any() and torch.equal(out[past], float("inf") * x64[past].sign())
+    scale = torch.exp2(s.cpu().double() - 127).expand(-1, 32)
+    assert (s.cpu() != 255).all() and torch.isfinite(out[~past]).all()
+    err = (out - x64).abs()
+    assert (err[~past] <= torch.maximum(2.0 ** -4 * x64.abs(), 2.0 ** -10 * scale)[~past]).all()
+
+
+@pytest.mark.parametrize("hint", [1, 300, 5000, 1 << 20])
+def test_gated_codes_at_the_border(hint):
+    """Gate and up sums about the border, and past bf16's range in fp32: the definition's codes from every kernel."""
+    announce("codes at the border", hint)
+    cs, n, k = [70, 3, 300], 64, 72
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    g = gen(hint)
+    a, w13 = torch.zeros(cap, k, dtype=BF), torch.zeros(3, 2 * n, k, dtype=BF)
+    a[:, 5] = 1
+    a[::2, 40] = 1
+    top = torch.tensor([0, 1, 100, 240, 247, 248, 249, 255], dtype=F64) * 2.0 ** 120
+    w13[:, :, 5] = (top[torch.randint(0, 8, (3, 2 * n), generator=g)] *
+                    (2.0 * torch.randint(0, 2, (3, 2 * n), generator=g) - 1)).to(BF)
+    w13[:, :32, 5] = 2.0 ** 100   # blocks without large ones
+    w13[:, :, 40] = (w13[:, :, 5].double().sign() * 0.875 * 2.0 ** 120).to(BF)
+    w13[:, :32, 40] = 0
+    ref = torch.zeros(cap, 2 * n, dtype=F64)   # two terms at most, whose sum fp32 holds exactly
+    for e, c in enumerate(cs):
+        r = slice(off[e], off[e] + c)
+        ref[r] = a[r].double() @ w13[e].double().T
+    assert float(ref.abs().max()) == 255.875 * 2.0 ** 120
+    _, h, h_s = run_fwd(a, w13, off, cs, "e4m3", hint)
+    assert rows_untouched(h, h_s, mask)
+    check_codes(h[mask.to(DEV)], h_s[mask.to(DEV)], ref[mask], "codes")
+    q, s, _ = encode(ref[mask])
+    out = sentinel((int(mask.sum()), 2 * n))
+    moe.moe_checkpoint_restore(h[mask.to(DEV)], h_s[mask.to(DEV)], out)
+    assert torch.equal(out.cpu().double(), torch.where(ref[mask].abs() >= BORDER, float("inf") * ref[mask].sign(),
+                                                       decode(q, s)))

@@ -125,7 +125,10 @@ __device__ __forceinline__ float quant_group16(const float (&x)[8], uint2& codes
 // The scale of 32 values in 8 bits (E8M0: byte b stands for 2^(b - 127)): the
 // least power of two that brings the largest magnitude, as fp32 bits m, to 448
 // (1.75 * 2^8) or below, but at least 2^-117, so that every restored value is
-// a normal number in bf16, and 255 (NaN) where m is an infinity or a NaN.
+// a normal number in bf16, and 255 (NaN) where m is an infinity or a NaN.  At
+// the largest scale, 2^120, magnitudes from 248 * 2^120 on round to 256 * 2^120,
+// which is past fp32 and bf16: they come back infinite, as a value past the
+// range does in any rounding to nearest.
 __device__ __forceinline__ uint32_t e8m0_of(uint32_t m) {
     const int e = (int)((m + 0x1fffffu) >> 23) - 8;
     return m >= 0x7f800000u ? 255u : (uint32_t)max(e, 10);
