@@ -450,7 +450,13 @@ int moe_unpermute_weight_reduce_bwd(const uint16_t* dout, const uint16_t* y, int
  * 248 * 2^120 (3.3e38; bf16's eight largest finite values 0x7f78..0x7f7f) up
  * to the largest fp32 value get the code of 2^128 and come back as infinities
  * of their sign, alone in their block.  A block that holds an infinity or a
- * NaN has b = 255 and is NaN throughout. */
+ * NaN has b = 255 and is NaN throughout.
+ * Where 8 bits are made of a product's fp32 sums, a sum within its own fp32
+ * error of the border between two codes (or two scales) may get either: the
+ * kernels add in different orders, and the sizes and rows_hint choose the
+ * kernel.  Such a value moves by one step of its code (2^-3 of itself at most;
+ * small values 2^-9 of the scale), and with it the gradients taken at it; one
+ * kernel gives the same codes every time. */
 
 /* x [rows,width] bf16 -> codes q [rows,width], scales [rows,width/32].
  * width: positive multiple of 32 up to 65536. */

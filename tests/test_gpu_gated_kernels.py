@@ -6,8 +6,9 @@ import torch
 
 import unpermute_count_expert_amd as moe
 from tests.gpu_helpers import announce
-from tests.test_gpu_bf16_experts import BF, DEV, F64, gen, segments, sentinel, valid_mask
-from tests.test_gpu_gated_experts import check_codes, decode, encode, rows_untouched, run_checkpoint, run_fwd
+from tests.test_gpu_bf16_experts import BF, DEV, F64, bf, gen, segments, sentinel, valid_mask
+from tests.test_gpu_gated_experts import (F8, check_codes, decode, encode, nearest_codes, rows_untouched, run_checkpoint,
+                                          run_fwd, scale_bytes)
 
 BORDER = 248 * 2.0 ** 120   # halfway between the last code that is finite at the largest scale and 2^128
 
@@ -67,3 +68,31 @@ def test_gated_codes_at_the_border(hint):
     moe.moe_checkpoint_restore(h[mask.to(DEV)], h_s[mask.to(DEV)], out)
     assert torch.equal(out.cpu().double(), torch.where(ref[mask].abs() >= BORDER, float("inf") * ref[mask].sign(),
                                                        decode(q, s)))
+
+
+@pytest.mark.parametrize("hint", [1, 300, 5000, 1 << 20])
+@pytest.mark.parametrize("n,k", [(32, 72), (160, 136), (288, 1032)])
+def test_gated_codes_differ_only_at_borders(n, k, hint):
+    """The code of a sum is the nearest one of a value within the sum's fp32 error, under the scale of a largest
+    magnitude within it, and the same in every run."""
+    announce("codes at borders", n, k, hint)
+    cs = [63, 0, 65, 1, 130, 290]
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    g = gen(n + k)
+    a, w13 = bf((cap, k), g), bf((len(cs), 2 * n, k), g, 4 * k ** -0.5)
+    _, h, h_s = run_fwd(a, w13, off, cs, "e4m3", hint)
+    _, h2, h_s2 = run_fwd(a, w13, off, cs, "e4m3", hint)
+    assert torch.equal(h, h2) and torch.equal(h_s, h_s2)
+    ref, err = torch.zeros(cap, 2 * n, dtype=F64), torch.zeros(cap, 2 * n, dtype=F64)
+    for e, c in enumerate(cs):
+        r = slice(off[e], off[e] + c)
+        ae, we = a[r].double(), w13[e].double()
+        ref[r], err[r] = ae @ we.T, k * 2.0 ** -23 * (ae.abs() @ we.abs().T)
+    ref, err, q, s = ref[mask], err[mask], h.cpu()[mask], h_s.cpu()[mask].int()
+    low = (ref.abs() - err).clamp(min=0)
+    assert (scale_bytes(low).int() <= s).all() and (s <= scale_bytes(ref.abs() + err).int()).all()
+    scale = torch.exp2(s.double() - 127).repeat_interleave(32, -1)
+    nearest = lambda v: nearest_codes((v / scale).clamp(-448, 448)).view(F8).double()
+    got = q.view(F8).double()
+    assert (nearest(ref - err) <= got).all() and (got <= nearest(ref + err)).all()
