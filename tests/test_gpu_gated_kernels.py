@@ -6,7 +6,7 @@ import torch
 
 import unpermute_count_expert_amd as moe
 from tests.gpu_helpers import announce
-from tests.test_gpu_bf16_experts import BF, DEV, F64, bf, gen, segments, sentinel, valid_mask
+from tests.test_gpu_bf16_experts import BF, DEV, F64, I32, bf, gen, i32, segments, sentinel, valid_mask
 from tests.test_gpu_gated_experts import (F8, check_codes, decode, encode, nearest_codes, rows_untouched, run_checkpoint,
                                           run_fwd, scale_bytes)
 
@@ -96,3 +96,89 @@ def test_gated_codes_differ_only_at_borders(n, k, hint):
     nearest = lambda v: nearest_codes((v / scale).clamp(-448, 448)).view(F8).double()
     got = q.view(F8).double()
     assert (nearest(ref - err) <= got).all() and (got <= nearest(ref + err)).all()
+
+
+# ---- side by side -----------------------------------------------------------------------
+class Calls:
+    """Every entry point over every kernel's hints, with inputs and outputs of its own made beforehand: enqueue()
+    calls the library alone."""
+
+    def __init__(self, seed):
+        g = gen(seed)
+        cs, n, k, M, T, W = [170, 0, 3, 600, 65, 1000], 544, 1032, 700, 3, 2048
+        off, cap = segments(cs, 16)
+        E, out = len(cs), []
+
+        def dev(t):
+            return t.to(DEV)
+
+        def result(*shape, dtype=BF):
+            out.append(torch.zeros(shape, dtype=dtype, device=DEV))
+            return out[-1]
+        U, F = torch.uint8, torch.float32
+        O, Cn = i32(off), i32(cs)
+        a, w13, dy, w2 = (dev(bf(s, g)) for s in ((cap, k), (E, 2 * n, k), (cap, k), (E, k, n)))
+        rw, x, tw = dev(torch.rand(cap, generator=g)), dev(bf((M, W), g)), dev(torch.rand((M, T), generator=g))
+        inv = dev(torch.randperm(cap, generator=g)[torch.arange(M * T) % cap].reshape(M, T).to(I32))
+        inv[M // 2:] = -1   # a row belongs to one pair
+        assert (M // 2) * T <= cap
+        table = dev(torch.randn((cap, 9), generator=g))
+        self.out, self.steps = out, []
+        add = lambda f, *args: self.steps.append(lambda: f(*args))
+        for hint in (1, 300, 3000, 30000, 1 << 20):
+            h, q, s = result(cap, 2 * n), result(cap, 2 * n, dtype=U), result(cap, n // 16, dtype=U)
+            add(moe.moe_grouped_gemm_bf16_silu_mul, a, w13, O, Cn, result(cap, n), None, None, hint)
+            add(moe.moe_grouped_gemm_bf16_silu_mul, a, w13, O, Cn, result(cap, n), h, None, hint)
+            add(moe.moe_grouped_gemm_bf16_silu_mul, a, w13, O, Cn, result(cap, n), q, s, hint)
+            add(moe.moe_grouped_gemm_bf16_dgrad_silu_mul, dy, w2, O, Cn, q, result(cap, 2 * n), result(cap, n), s, rw,
+                result(cap, -(-n // 64), dtype=F), hint)
+            add(moe.moe_grouped_gemm_bf16_dgrad_silu_mul, dy, w2, O, Cn, h, h, None, None, rw, None, hint)
+        xq, xs = result(M, W, dtype=U), result(M, W // 32, dtype=U)
+        add(moe.moe_checkpoint, x, xq, xs)
+        add(moe.moe_checkpoint_restore, xq, xs, result(cap, W), inv)
+        add(moe.moe_permute_rows, x, inv, result(cap, W), tw, result(cap, dtype=F))
+        add(moe.moe_topk_weights_bwd, table, inv, result(M, T, dtype=F))
+
+    def clear(self):
+        for t in self.out:
+            t.zero_()
+
+
+def test_gated_entry_points_of_two_streams_in_flight_together():
+    """Two streams held back until both are filled: their kernels run beside each other and give the bits of each
+    alone."""
+    work = [Calls(71), Calls(72)]
+    want = []
+    for w in work:
+        for step in w.steps:
+            step()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in w.out])
+    streams = [torch.cuda.Stream() for _ in work]
+    big = torch.ones(1 << 28, device=DEV)
+    for turn in range(4):
+        for w in work:
+            w.clear()
+        torch.cuda.synchronize()
+        for _ in range(40):   # some milliseconds, in which the host fills both streams
+            big.mul_(1.0)
+        held = torch.cuda.Event()
+        held.record()
+        span = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in work]
+        for st, ev in zip(streams, span):
+            st.wait_event(held)
+            ev[0].record(st)
+        order = range(len(work[0].steps))
+        for j in order:   # in step, or two hints (five calls each) apart, so that different kernels meet
+            for w, st, at in zip(work, streams, (j, j if turn % 2 else (j + 10) % len(order))):
+                with torch.cuda.stream(st):
+                    w.steps[at]()
+        filled_early = not held.query()
+        for st, ev in zip(streams, span):
+            ev[1].record(st)
+        torch.cuda.synchronize()
+        assert filled_early, "the streams ran while they were filled"
+        assert span[0][0].elapsed_time(span[1][1]) > 0 and span[1][0].elapsed_time(span[0][1]) > 0
+        for w, ref in zip(work, want):
+            for i, (t, r) in enumerate(zip(w.out, ref)):
+                assert torch.equal(t.view(torch.uint8), r.view(torch.uint8)), (turn, i)
