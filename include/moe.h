@@ -517,6 +517,24 @@ int moe_grouped_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w2,
                                          const float* row_weights, uint16_t* dh, uint16_t* act, float* dots,
                                          void* stream);
 
+/* How a grouped product on bf16 rows runs: *tile_rows the rows of its kernel's
+ * tiles (16: the kernel for a few rows an expert, 64 x 128 tiles, 128 x 256 or
+ * 256 x 256), *staggered 1 where neighbouring tiles start the contraction a
+ * step apart.  op MOE_GEMM_BF16_*; n and k the two widths as its entry point
+ * takes them, in that order (n_out and k_in; n and k_in with SiLU-mul; k_out
+ * and n of the gradient through it); rows_hint > 0 (where a call gives none it
+ * is cap_rows; the gradient by the weights does not read it); num_cus the
+ * compute units, 0 for the current device's.  Kernels add in different orders:
+ * results of calls with the same kernel are equal, others equal to rounding.
+ * Either output pointer may be NULL. */
+#define MOE_GEMM_BF16_FORWARD 0
+#define MOE_GEMM_BF16_DGRAD 1
+#define MOE_GEMM_BF16_WGRAD 2
+#define MOE_GEMM_BF16_SILU_MUL 3
+#define MOE_GEMM_BF16_DGRAD_SILU_MUL 4
+int moe_grouped_gemm_bf16_plan_info(int32_t op, int32_t El, int32_t n, int32_t k, int64_t rows_hint, int32_t num_cus,
+                                    int32_t* tile_rows, int32_t* staggered);
+
 /* dweights[t,k] = sum_i dots[inv_perm[t,k], i] where 0 <= inv_perm[t,k] < rows,
  * else 0, in a fixed order.  dots [rows,num_dots] fp32, 1 <= num_dots <= 1024,
  * inv_perm and dweights [Mc,topk]. */

@@ -5,12 +5,31 @@ import pytest
 import torch
 
 import unpermute_count_expert_amd as moe
+from tests import test_gpu_gated_experts as whole
 from tests.gpu_helpers import announce
-from tests.test_gpu_bf16_experts import BF, DEV, F64, I32, bf, gen, i32, segments, sentinel, valid_mask
-from tests.test_gpu_gated_experts import (F8, check_codes, decode, encode, nearest_codes, rows_untouched, run_checkpoint,
-                                          run_fwd, scale_bytes)
+from tests.test_gpu_bf16_experts import (BF, DEV, F64, I32, TINY, bf, gen, i32, poison, segments, sentinel, valid_mask)
+from tests.test_gpu_gated_experts import (F8, at_16_bytes, bwd_reference, check_codes, decode, encode, kept_rows,
+                                          nearest_codes, rows_untouched, run_checkpoint, run_fwd, scale_bytes, silu,
+                                          within)
 
 BORDER = 248 * 2.0 ** 120   # halfway between the last code that is finite at the largest scale and 2^128
+
+# Rows of 40 experts, with which every kernel is reached by the rows given, at widths that end inside a tile and inside
+# its parts of 64 and 32 columns
+ROWS = [0, 1, 63, 64, 65, 16, 0, 128, 130, 3, 257, 2, 0, 300, 17] + [0, 5] * 12 + [31]
+KERNELS = {"forward": ["16", "64 staggered", "128 staggered", "256 staggered", "256"], "backward": ["16", "64", "128", "256"]}
+CASES = [(op, kernel) for op in KERNELS for kernel in KERNELS[op]]
+N_OF, K_ODD = {"none": 1000, "bf16": 1000, "e4m3": 992}, 520
+
+
+def hint_of(op, kernel, n, k, E=len(ROWS)):
+    """The least power of 2^(1/8) rows for which the call takes the kernel."""
+    at = (moe.MOE_GEMM_BF16_SILU_MUL, E, n, k) if op == "forward" else (moe.MOE_GEMM_BF16_DGRAD_SILU_MUL, E, k, n)
+    for i in range(31 * 8):
+        p = moe.moe_grouped_gemm_bf16_plan_info(*at, int(2 ** (i / 8)))
+        if f"{p['tile_rows']}{' staggered' if p['staggered'] else ''}" == kernel:
+            return int(2 ** (i / 8))
+    raise AssertionError(f"no rows give {kernel} for {op} of {at}")
 
 
 # ---- 8 bits at the end of the range -----------------------------------------------------
@@ -100,12 +119,12 @@ def test_gated_codes_differ_only_at_borders(n, k, hint):
 
 # ---- side by side -----------------------------------------------------------------------
 class Calls:
-    """Every entry point over every kernel's hints, with inputs and outputs of its own made beforehand: enqueue()
-    calls the library alone."""
+    """Every entry point and each of its kernels, with inputs and outputs made beforehand: the steps call the library
+    alone."""
 
     def __init__(self, seed):
         g = gen(seed)
-        cs, n, k, M, T, W = [170, 0, 3, 600, 65, 1000], 544, 1032, 700, 3, 2048
+        cs, n, k, M, T, W = ROWS, 992, 520, 700, 3, 2048
         off, cap = segments(cs, 16)
         E, out = len(cs), []
 
@@ -121,18 +140,20 @@ class Calls:
         rw, x, tw = dev(torch.rand(cap, generator=g)), dev(bf((M, W), g)), dev(torch.rand((M, T), generator=g))
         inv = dev(torch.randperm(cap, generator=g)[torch.arange(M * T) % cap].reshape(M, T).to(I32))
         inv[M // 2:] = -1   # a row belongs to one pair
-        assert (M // 2) * T <= cap
-        table = dev(torch.randn((cap, 9), generator=g))
+        assert M // 2 * T <= cap
+        table = dev(torch.randn((cap, 16), generator=g))
         self.out, self.steps = out, []
         add = lambda f, *args: self.steps.append(lambda: f(*args))
-        for hint in (1, 300, 3000, 30000, 1 << 20):
+        up, down = ([hint_of(op, kernel, n, k) for kernel in KERNELS[op]] for op in ("forward", "backward"))
+        for i, hint in enumerate(up):
+            back = down[i % len(down)]
             h, q, s = result(cap, 2 * n), result(cap, 2 * n, dtype=U), result(cap, n // 16, dtype=U)
             add(moe.moe_grouped_gemm_bf16_silu_mul, a, w13, O, Cn, result(cap, n), None, None, hint)
             add(moe.moe_grouped_gemm_bf16_silu_mul, a, w13, O, Cn, result(cap, n), h, None, hint)
             add(moe.moe_grouped_gemm_bf16_silu_mul, a, w13, O, Cn, result(cap, n), q, s, hint)
             add(moe.moe_grouped_gemm_bf16_dgrad_silu_mul, dy, w2, O, Cn, q, result(cap, 2 * n), result(cap, n), s, rw,
-                result(cap, -(-n // 64), dtype=F), hint)
-            add(moe.moe_grouped_gemm_bf16_dgrad_silu_mul, dy, w2, O, Cn, h, h, None, None, rw, None, hint)
+                result(cap, -(-n // 64), dtype=F), back)
+            add(moe.moe_grouped_gemm_bf16_dgrad_silu_mul, dy, w2, O, Cn, h, h, None, None, rw, None, back)
         xq, xs = result(M, W, dtype=U), result(M, W // 32, dtype=U)
         add(moe.moe_checkpoint, x, xq, xs)
         add(moe.moe_checkpoint_restore, xq, xs, result(cap, W), inv)
@@ -169,7 +190,7 @@ def test_gated_entry_points_of_two_streams_in_flight_together():
             st.wait_event(held)
             ev[0].record(st)
         order = range(len(work[0].steps))
-        for j in order:   # in step, or two hints (five calls each) apart, so that different kernels meet
+        for j in order:   # in step, or two kernels (five calls each) apart, so that different kernels meet
             for w, st, at in zip(work, streams, (j, j if turn % 2 else (j + 10) % len(order))):
                 with torch.cuda.stream(st):
                     w.steps[at]()
@@ -182,3 +203,224 @@ def test_gated_entry_points_of_two_streams_in_flight_together():
         for w, ref in zip(work, want):
             for i, (t, r) in enumerate(zip(w.out, ref)):
                 assert torch.equal(t.view(torch.uint8), r.view(torch.uint8)), (turn, i)
+
+
+# ---- each kernel -------------------------------------------------------------------------
+class Guarded:
+    """Tensors inside larger ones, whose margins (4 KB on either side) nothing writes."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, *shape, dtype=BF):
+        size = torch.empty(0, dtype=dtype).element_size()
+        whole = torch.full((torch.Size(shape).numel() * size + 8192,), 0x7b, dtype=torch.uint8, device=DEV)
+        self.all.append(whole)
+        return whole[4096:-4096].view(dtype).view(shape)
+
+    def intact(self):
+        return all(bool((w[:4096] == 0x7b).all() and (w[-4096:] == 0x7b).all()) for w in self.all)
+
+
+def outputs(op, keep, cap, n, new):
+    U, F = torch.uint8, torch.float32
+    if op == "backward":
+        return [new(cap, 2 * n), new(cap, n), new(cap, -(-n // 64), dtype=F)]
+    kept = {"none": [], "bf16": [new(cap, 2 * n)], "e4m3": [new(cap, 2 * n, dtype=U), new(cap, n // 16, dtype=U)]}[keep]
+    return [new(cap, n)] + kept
+
+
+def call(op, rows, w, off, cs, out, hint, kept=(None, None), weights=None):
+    if op == "forward":
+        moe.moe_grouped_gemm_bf16_silu_mul(rows, w, off, cs, *out, rows_hint=hint)
+    else:
+        moe.moe_grouped_gemm_bf16_dgrad_silu_mul(rows, w, off, cs, kept[0], out[0], out[1], kept[1], weights, out[2], hint)
+
+
+def inputs(op, keep, cap, n, g, E=len(ROWS)):
+    """(rows, weights of the experts, kept gate and up rows with scales, router weights) on the GPU; small integers in
+    the products, whose sums fp32 holds exactly, so that every kernel gives the same bits."""
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g).to(BF)
+    rows = ints(cap, K_ODD).to(DEV)
+    if op == "forward":
+        return rows, ints(E, 2 * n, K_ODD).to(DEV), (None, None), None
+    h = bf((cap, 2 * n), g, 3.0)
+    if keep == "e4m3":
+        q, s, _ = encode(h.double())
+        kept = q.to(DEV), s.to(DEV)
+    else:
+        kept = h.to(DEV), None
+    return rows, ints(E, K_ODD, n).to(DEV), kept, (torch.rand(cap, generator=g) + 0.5).to(DEV)
+
+
+def equal_rows(x, y, mask):
+    m = mask.to(DEV)
+    return all(torch.equal(a[m].view(torch.uint8), b[m].view(torch.uint8)) for a, b in zip(x, y))
+
+
+KEEPS = {"forward": ("none", "bf16", "e4m3"), "backward": ("bf16", "e4m3")}
+
+
+@pytest.mark.parametrize("op,kernel,keep", [(*c, keep) for c in CASES for keep in KEEPS[c[0]]])
+def test_each_kernel_at_odd_widths(op, kernel, keep):
+    """Random rows at widths that end inside a tile, NaN in the rows of no expert, against 64 bits; margins intact."""
+    announce("each kernel", op, kernel, keep)
+    n, k, new, cs = N_OF[keep], K_ODD, Guarded(), ROWS
+    hint = hint_of(op, kernel, n, k)
+    off, cap = segments(cs, 16)
+    mask = valid_mask(cs, off, cap)
+    g = gen(int(kernel.split()[0]) + n)
+    out = outputs(op, keep, cap, n, new)
+    O, Cn, E = i32(off), i32(cs), len(cs)
+    if op == "forward":
+        a, w = bf((cap, k), g), bf((E, 2 * n, k), g, 4 * k ** -0.5)
+        call(op, poison(a, mask).to(DEV), w.to(DEV), O, Cn, out, hint)
+    else:
+        a, w = bf((cap, k), g, 0.5), bf((E, k, n), g, k ** -0.5)
+        H, HS, h = kept_rows(cap, n, keep, g, mask)
+        rw = torch.rand(cap, generator=g) * 2 - 0.5
+        RW = torch.where(mask, rw, float("nan"))
+        call(op, poison(a, mask).to(DEV), w.to(DEV), O, Cn, out, hint, (H, HS), RW.to(DEV))
+    torch.cuda.synchronize()
+    assert new.intact()
+    for t in out:
+        assert (t.cpu()[~mask].view(torch.uint8) == 0x7b).all()
+    nd = -(-n // 64)
+    for e, c in enumerate(cs):
+        if c == 0:
+            continue
+        r = slice(off[e], off[e] + c)
+        ae, we = a[r].double(), w[e].double().T if op == "forward" else w[e].double()
+        ref, err = ae @ we, k * 2.0 ** -23 * (ae.abs() @ we.abs())
+        if op == "backward":
+            b = bwd_reference(h[r], ref, err, rw[r].double(), n)
+            for name, got in (("act", out[1][r]), ("dg", out[0][r, :n]), ("du", out[0][r, n:])):
+                v, tol = b[name]
+                within(got, v, tol + 2.0 ** -8 * (v.abs() + tol) + TINY, name)
+            v, tol = b["dot"]
+            pad = lambda t: torch.nn.functional.pad(t, (0, nd * 64 - n)).reshape(c, nd, 64)
+            within(out[2][r], pad(v).sum(-1), pad(tol).sum(-1) + 64 * 2.0 ** -23 * pad(v.abs() + tol).sum(-1) + TINY, "dots")
+            continue
+        gr, ur, ge, ue = ref[:, :n], ref[:, n:], err[:, :n], err[:, n:]
+        want = silu(gr) * ur
+        tol = 1.1 * ge * ur.abs() + silu(gr).abs() * ue + 1.1 * ge * ue
+        within(out[0][r], want, tol + (2.0 ** -8 + 2.0 ** -22 * (4 + gr.abs())) * (want.abs() + tol) + TINY, "act")
+        if keep == "bf16":
+            within(out[1][r], ref, err + 2.0 ** -8 * (ref.abs() + err) + TINY, "h")
+        if keep == "e4m3":
+            scale = ((ref.abs() + err).reshape(c, -1, 32).amax(-1) / 224).repeat_interleave(32, -1)
+            within(decode(out[1][r].cpu(), out[2][r].cpu()), ref,
+                   err + torch.maximum(2.0 ** -4 * (ref.abs() + err), 2.0 ** -10 * scale), "h in 8 bits")
+
+
+@pytest.mark.parametrize("op,keep", [(op, keep) for op in KERNELS for keep in KEEPS[op]])
+def test_kernels_agree_where_sums_are_exact(op, keep):
+    """Sums that fp32 holds exactly: the same bits from every kernel, from calls with other rows given that take the
+    same one, and from tensors that start 16 bytes into a line."""
+    announce("kernels agree", op, keep)
+    n = N_OF[keep]
+    off, cap = segments(ROWS, 16)
+    mask = valid_mask(ROWS, off, cap)
+    rows, w, kept, weights = inputs(op, keep, cap, n, gen(n))
+    O, Cn, first = i32(off), i32(ROWS), None
+    for kernel in KERNELS[op]:
+        hint, new = hint_of(op, kernel, n, K_ODD), Guarded()
+        out = outputs(op, keep, cap, n, new)
+        call(op, rows, w, O, Cn, out, hint, kept, weights)
+        first = first or out
+        if op == "backward":   # the sums of 64 columns' products are rounded: in each kernel's order
+            assert equal_rows(out[:2], first[:2], mask)
+        else:
+            assert equal_rows(out, first, mask)
+        moved = [t if t is None else at_16_bytes(t) for t in (rows, w, O, Cn, *kept, weights)]
+        there = [at_16_bytes(t) for t in outputs(op, keep, cap, n, new)]
+        call(op, *moved[:4], there, hint, tuple(moved[4:6]), moved[6])
+        assert all(t.data_ptr() % 256 == 16 for t in there) and equal_rows(out, there, mask) and new.intact()
+
+
+def cut_rows(off, cs, cap):
+    """The rows of each expert as documented: its segment cut at the next one's start and at the buffer."""
+    rows = []
+    for e, c in enumerate(cs):
+        end = min(max(off[e + 1], 0), cap)
+        lo = min(max(off[e], 0), end)
+        rows.append(range(lo, min(lo + max(c, 0), end)))
+    return rows
+
+
+@pytest.mark.parametrize("op,kernel,keep", [(*c, keep) for c in CASES for keep in ("bf16", "e4m3")])
+def test_each_kernel_cuts_inconsistent_segments(op, kernel, keep):
+    """Counts past their slot, negative counts and offsets out of order or past the buffer: rows outside every segment
+    and the memory around the outputs stay as they are, and segments that do not overlap have their values."""
+    announce("cut segments", op, kernel, keep)
+    n, E = N_OF[keep], len(ROWS)
+    hint = hint_of(op, kernel, n, K_ODD)
+    off, cap = segments(ROWS, 16)
+    rows, w, kept, weights = inputs(op, keep, cap, n, gen(n + 1))
+
+    def run(o, c):
+        new = Guarded()
+        out = outputs(op, keep, cap, n, new)
+        call(op, rows, w, i32(o), i32(c), out, hint, kept, weights)
+        torch.cuda.synchronize()
+        assert new.intact()
+        named = torch.zeros(cap, dtype=torch.bool)
+        for r in cut_rows(o, c, cap):
+            named[r.start:r.stop] = True
+        for t in out:
+            assert (t.cpu()[~named].view(torch.uint8) == 0x7b).all()
+        return out, named
+
+    long = [c if e % 3 else 1 << 20 for e, c in enumerate(ROWS)]
+    long[4], long[8] = -3, -(1 << 31)
+    got, named = run(off, long)
+    plain, same = run(off, [len(r) for r in cut_rows(off, long, cap)])
+    assert torch.equal(named, same) and equal_rows(got, plain, named)
+    run([-7] + [cap + 5] * 20 + [40] * 20, [200] * E)
+    run([500 * (e % 3) - 9 * e for e in range(E + 1)], ROWS)
+    run([cap - 3 + e // 20 for e in range(E + 1)], [1 << 30] * E)
+
+
+@pytest.mark.parametrize("op,kernel,keep", [(*c, keep) for c in CASES for keep in ("bf16", "e4m3")])
+def test_each_kernel_keeps_non_finite_values_in_their_rows(op, kernel, keep):
+    announce("non-finite", op, kernel, keep)
+    n = N_OF[keep]
+    hint = hint_of(op, kernel, n, K_ODD)
+    off, cap = segments(ROWS, 16)
+    mask = valid_mask(ROWS, off, cap)
+    rows, w, kept, weights = inputs(op, keep, cap, n, gen(n + 2))
+    bad = [off[3] + 40, off[10] + 256, off[13] + 128, off[1]]   # inside a tile, an expert's last row, its only one
+    out = outputs(op, keep, cap, n, Guarded())
+    call(op, rows, w, i32(off), i32(ROWS), out, hint, kept, weights)
+    planted = rows.clone()
+    for i, b in enumerate(bad):
+        planted[b, (5, 519, 100, 0)[i]] = float("inf") if i % 2 else float("nan")
+    planted[~mask.to(DEV)] = float("nan")
+    if op == "backward":   # the kept rows of no expert as well
+        h, h_s = kept[0].clone(), kept[1]
+        if keep == "bf16":
+            h[~mask.to(DEV)] = float("nan")
+        else:
+            h_s = h_s.clone()
+            h_s[~mask.to(DEV)] = 255
+        kept = h, h_s
+    got = outputs(op, keep, cap, n, Guarded())
+    call(op, planted, w, i32(off), i32(ROWS), got, hint, kept, weights)
+    clean = mask.clone()
+    clean[bad] = False
+    assert equal_rows(got, out, clean)
+    what = got[0] if op == "backward" else got[2] if keep == "e4m3" else got[1]
+    marked = what.cpu()[bad] == 255 if what.dtype == torch.uint8 else ~torch.isfinite(what.cpu()[bad].float())
+    assert marked.any(1).all()
+
+
+@pytest.mark.parametrize("up,down", [("64 staggered", "64"), ("128 staggered", "128"), ("256 staggered", "128")])
+def test_each_kernel_past_32_bits(up, down):
+    """test_gated_past_32_bits with rows given that take these kernels (its own take the others)."""
+    at = 140, 2048, 4096
+    rows = {hint_of("forward", up, *at[1:], at[0]), hint_of("backward", down, *at[1:], at[0])}
+    name = lambda p: f"{p['tile_rows']}{' staggered' if p['staggered'] else ''}"
+    hint = max(rows)   # both kernels' ranges have begun: the first one's has not ended
+    assert name(moe.moe_grouped_gemm_bf16_plan_info(moe.MOE_GEMM_BF16_SILU_MUL, *at, hint)) == up
+    assert name(moe.moe_grouped_gemm_bf16_plan_info(moe.MOE_GEMM_BF16_DGRAD_SILU_MUL, 140, 4096, 2048, hint)) == down
+    whole.test_gated_past_32_bits(hint)

@@ -16,5 +16,7 @@ from ._lib import (MOE_ACT_IDENTITY, MOE_ACT_SILU_MUL, MoeError, MoeProblem, loa
                    moe_permute_bf16, moe_grouped_gemm_bf16, moe_grouped_gemm_bf16_dgrad, moe_grouped_gemm_bf16_wgrad,
                    moe_silu_mul, moe_silu_mul_bwd, moe_unpermute_weight_reduce_bwd, moe_grad_workspace_size,
                    moe_grad_sumsq, moe_grad_clip, moe_checkpoint, moe_checkpoint_restore, moe_permute_rows,
-                   moe_grouped_gemm_bf16_silu_mul, moe_grouped_gemm_bf16_dgrad_silu_mul, moe_topk_weights_bwd)
+                   moe_grouped_gemm_bf16_silu_mul, moe_grouped_gemm_bf16_dgrad_silu_mul, moe_topk_weights_bwd,
+                   moe_grouped_gemm_bf16_plan_info, MOE_GEMM_BF16_FORWARD, MOE_GEMM_BF16_DGRAD, MOE_GEMM_BF16_WGRAD,
+                   MOE_GEMM_BF16_SILU_MUL, MOE_GEMM_BF16_DGRAD_SILU_MUL)
 from .layer import MoeLayer, MoeTrainLayer  # noqa: F401

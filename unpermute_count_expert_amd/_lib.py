@@ -54,7 +54,7 @@ EXPORTS = ["moe_status_string", "moe_last_error", "moe_max_rows", "moe_grouped_g
            "moe_grouped_gemm_bf16_wgrad", "moe_silu_mul", "moe_silu_mul_bwd", "moe_unpermute_weight_reduce_bwd",
            "moe_grad_workspace_size", "moe_grad_sumsq", "moe_grad_clip", "moe_checkpoint", "moe_checkpoint_restore",
            "moe_permute_rows", "moe_grouped_gemm_bf16_silu_mul", "moe_grouped_gemm_bf16_dgrad_silu_mul",
-           "moe_topk_weights_bwd"]
+           "moe_topk_weights_bwd", "moe_grouped_gemm_bf16_plan_info"]
 
 _lib = None
 
@@ -113,6 +113,7 @@ def load() -> C.CDLL:
         L.moe_grouped_gemm_bf16_silu_mul.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, P, P, P, P]
         L.moe_grouped_gemm_bf16_dgrad_silu_mul.argtypes = [P, P, P, P, I32, I64, I32, I32, I64, P, P, P, P, P, P, P]
         L.moe_topk_weights_bwd.argtypes = [P, I32, I64, P, I64, I32, P, P]
+        L.moe_grouped_gemm_bf16_plan_info.argtypes = [I32, I32, I32, I32, I64, I32, C.POINTER(I32), C.POINTER(I32)]
         L.moe_noalloc_scratch_bytes.argtypes = []; L.moe_noalloc_scratch_bytes.restype = SZ
         for name in EXPORTS:
             if name not in ("moe_status_string", "moe_last_error", "moe_max_rows", "moe_grouped_gemm_tile_rows",
@@ -758,6 +759,19 @@ def moe_grouped_gemm_bf16_dgrad_silu_mul(dy, w2, expert_offsets, counts, h, dh, 
                                                        cap_rows, k, n, rows_hint, _ptr(h), _ptr(h_s),
                                                        _ptr(row_weights), _ptr(dh), _ptr(act), _ptr(dots),
                                                        _stream(stream)), "moe_grouped_gemm_bf16_dgrad_silu_mul")
+
+
+MOE_GEMM_BF16_FORWARD, MOE_GEMM_BF16_DGRAD, MOE_GEMM_BF16_WGRAD = 0, 1, 2
+MOE_GEMM_BF16_SILU_MUL, MOE_GEMM_BF16_DGRAD_SILU_MUL = 3, 4
+
+
+def moe_grouped_gemm_bf16_plan_info(op: int, El: int, n: int, k: int, rows_hint: int, num_cus: int = 0) -> dict:
+    """The kernel that a grouped product on bf16 rows takes: tile_rows (16, 64, 128 or 256) and staggered.  op
+    MOE_GEMM_BF16_*, n and k its widths in its entry point's order, num_cus 0: the current device's."""
+    v = [C.c_int32(), C.c_int32()]
+    _check(load().moe_grouped_gemm_bf16_plan_info(op, El, n, k, rows_hint, num_cus, *[C.byref(x) for x in v]),
+           "moe_grouped_gemm_bf16_plan_info")
+    return dict(tile_rows=v[0].value, staggered=bool(v[1].value))
 
 
 def moe_topk_weights_bwd(dots, inv_perm, dweights, stream=None):

@@ -1371,6 +1371,27 @@ int moe_grouped_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w2,
     return MOE_OK;
 }
 
+int moe_grouped_gemm_bf16_plan_info(int32_t op, int32_t El, int32_t n, int32_t k, int64_t rows_hint, int32_t num_cus,
+                                    int32_t* tile_rows, int32_t* staggered) {
+    REQUIRE(op >= MOE_GEMM_BF16_FORWARD && op <= MOE_GEMM_BF16_DGRAD_SILU_MUL, MOE_ERR_INVALID_ARG, "op=%d", op);
+    REQUIRE(El >= 1 && El <= moe::kMaxLocalExperts, MOE_ERR_SHAPE, "El=%d outside [1,1024]", El);
+    const int32_t n_max = op == MOE_GEMM_BF16_SILU_MUL ? 32768 : 65536;
+    const int32_t k_max = op == MOE_GEMM_BF16_DGRAD_SILU_MUL ? 32768 : 65536;
+    REQUIRE(n > 0 && n % 8 == 0 && n <= n_max, MOE_ERR_SHAPE, "n=%d is not a positive multiple of 8 up to %d", n, n_max);
+    REQUIRE(k > 0 && k % 8 == 0 && k <= k_max, MOE_ERR_SHAPE, "k=%d is not a positive multiple of 8 up to %d", k, k_max);
+    REQUIRE(rows_hint > 0, MOE_ERR_SHAPE, "rows_hint=%lld", (long long)rows_hint);
+    REQUIRE(num_cus >= 0 && num_cus <= 65536, MOE_ERR_INVALID_ARG, "num_cus=%d", num_cus);
+    int cus = num_cus;
+    if (cus == 0) {
+        const int st = check_device(&cus);
+        if (st) return st;
+    }
+    const moe::GemmBf16Plan p = moe::gemm_bf16_plan(op, El, n, k, rows_hint, cus);
+    if (tile_rows) *tile_rows = p.tile_rows;
+    if (staggered) *staggered = p.staggered ? 1 : 0;
+    return MOE_OK;
+}
+
 int moe_topk_weights_bwd(const float* dots, int32_t num_dots, int64_t rows, const int32_t* inv_perm, int64_t Mc,
                          int32_t topk, float* dweights, void* stream) {
     REQUIRE(num_dots >= 1 && num_dots <= 1024, MOE_ERR_SHAPE, "num_dots=%d outside [1,1024]", num_dots);

@@ -114,7 +114,7 @@
 namespace moe {
 namespace {
 
-enum { kFwd = 0, kDgrad = 1, kWgrad = 2, kGated = 3, kGatedBwd = 4 };
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2, kGated = 3, kGatedBwd = 4 };   // MOE_GEMM_BF16_*
 enum { kKeepNone = 0, kKeepBf16 = 1, kKeepE4m3 = 2 };   // gate and up rows for the backward pass
 
 // What the gated products have besides: kGated writes h (and h_s), kGatedBwd
@@ -1405,23 +1405,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_few(const uint16_t* __restrict_
 // 128 rows, 59 with 256; 128 of 264 x 360, 16384 rows: 63 and 86; 128 of
 // 1536 x 2048, 32768 rows, bf16: 340 and 288).
 // Forward tiles turn (TURN) up to 208 rows per expert, 128-row ones always.
-template <int MODE, bool F32, bool ACC, int KEEP = kKeepNone>
-hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
-                  int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, void* out, int num_cus, hipStream_t s,
-                  Gate gate = {}) {
+template <int MODE>
+GemmBf16Plan choose(int El, int n_out, int k_in, int64_t rows_hint, int num_cus) {
     constexpr bool FWD = MODE == kFwd || MODE == kGated;
-    const unsigned grid = (unsigned)((num_cus + 7) / 8 * 8);   // the same number of blocks on each of the eight XCDs
-    auto tiles = [&](auto* kernel) {
-        kernel<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, out, gate);
-    };
     const double cus = num_cus;
     const int N = (FWD ? n_out : k_in) * (MODE == kGated ? 2 : 1);   // output columns; gate and up
     const int ntn = (N + BN - 1) / BN;                               // n-tiles
     if constexpr (MODE == kWgrad) {
         const double rounds1 = std::ceil((double)El * ((n_out + 127) / 128) * ntn / cus);
         const double rounds2 = std::ceil((double)El * ((n_out + 255) / 256) * ntn / cus);
-        if (3 * rounds1 <= 5 * rounds2) tiles(k_tiles<MODE, 1, F32, ACC, false, KEEP, false>);
-        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP, false>);
+        return {3 * rounds1 <= 5 * rounds2 ? 128 : 256, false};
     } else {
         constexpr int NC = FWD ? 32 : 64, KS = FWD ? 64 : 32;   // k_few's columns and step
         const int C = FWD ? k_in : n_out;
@@ -1456,19 +1449,41 @@ hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, 
             const double small = std::max(
                 3.0 + std::max(1.0, rounds0) * (GB ? 1.0 + 0.7 * ((C + BK - 1) / BK) : 3.0 + 0.8 * ((C + BK - 1) / BK)),
                 GB ? bytes * (0.9 + 0.06 * mtiles) : bytes * (0.95 + 0.06 * mtiles) - 2);
-            if (El <= kSmallExperts && small < std::min(std::max(few, bytes), std::max(walk, bytes + 1))) {
-                k_tiles<MODE, 1, F32, ACC, FWD, KEEP, true><<<kSmallBlocks * grid, kSmallThreads, 0, s>>>(
-                    a, b, offsets, counts, El, cap_rows, n_out, k_in, out, gate);
-                return hipGetLastError();
-            }
+            if (El <= kSmallExperts && small < std::min(std::max(few, bytes), std::max(walk, bytes + 1))) return {64, FWD};
         }
-        if (std::max(few, bytes) <= std::max(walk, bytes + 1))
+        if (std::max(few, bytes) <= std::max(walk, bytes + 1)) return {16, false};
+        if (low) return {128, FWD};
+        return {256, FWD && rows_hint < (int64_t)208 * El};
+    }
+}
+
+template <int MODE, bool F32, bool ACC, int KEEP = kKeepNone>
+hipError_t launch(const uint16_t* a, const uint16_t* b, const int32_t* offsets, const int32_t* counts, int El,
+                  int64_t cap_rows, int n_out, int k_in, int64_t rows_hint, void* out, int num_cus, hipStream_t s,
+                  Gate gate = {}) {
+    constexpr bool FWD = MODE == kFwd || MODE == kGated, G = MODE == kGated || MODE == kGatedBwd;
+    const unsigned grid = (unsigned)((num_cus + 7) / 8 * 8);   // the same number of blocks on each of the eight XCDs
+    auto tiles = [&](auto* kernel) {
+        kernel<<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in, out, gate);
+    };
+    const GemmBf16Plan plan = choose<MODE>(El, n_out, k_in, rows_hint, num_cus);
+    if constexpr (G) {
+        if (plan.tile_rows == 64) {
+            k_tiles<MODE, 1, F32, ACC, FWD, KEEP, true><<<kSmallBlocks * grid, kSmallThreads, 0, s>>>(
+                a, b, offsets, counts, El, cap_rows, n_out, k_in, out, gate);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (MODE != kWgrad) {
+        if (plan.tile_rows == 16) {
             k_few<MODE, KEEP><<<grid, kThreads, 0, s>>>(a, b, offsets, counts, El, cap_rows, n_out, k_in,
                                                         static_cast<uint16_t*>(out), gate);
-        else if (low) tiles(k_tiles<MODE, 1, F32, ACC, FWD, KEEP, false>);
-        else if (FWD && rows_hint < (int64_t)208 * El) tiles(k_tiles<MODE, 2, F32, ACC, FWD, KEEP, false>);
-        else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP, false>);
+            return hipGetLastError();
+        }
     }
+    if (plan.tile_rows == 128) tiles(k_tiles<MODE, 1, F32, ACC, FWD, KEEP, false>);
+    else if (plan.staggered) tiles(k_tiles<MODE, 2, F32, ACC, FWD, KEEP, false>);
+    else tiles(k_tiles<MODE, 2, F32, ACC, false, KEEP, false>);
     return hipGetLastError();
 }
 
@@ -1506,6 +1521,15 @@ hipError_t launch_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w
     auto* go = h_s ? launch<kGatedBwd, false, false, kKeepE4m3> : launch<kGatedBwd, false, false, kKeepBf16>;
     return go(dy, w2, offsets, counts, El, cap_rows, k_out, n, rows_hint, dh, num_cus, s,
               Gate{const_cast<void*>(h), const_cast<uint8_t*>(h_s), row_w, dots, act});
+}
+
+GemmBf16Plan gemm_bf16_plan(int op, int El, int n_out, int k_in, int64_t rows_hint, int num_cus) {
+    auto* choice = op == kFwd     ? choose<kFwd>
+                   : op == kDgrad ? choose<kDgrad>
+                   : op == kWgrad ? choose<kWgrad>
+                   : op == kGated ? choose<kGated>
+                                  : choose<kGatedBwd>;
+    return choice(El, n_out, k_in, rows_hint, num_cus);
 }
 
 }  // namespace moe

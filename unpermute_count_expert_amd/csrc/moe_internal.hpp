@@ -178,6 +178,15 @@ hipError_t launch_gemm_bf16_dgrad_silu_mul(const uint16_t* dy, const uint16_t* w
                                            int64_t rows_hint, const void* h, const uint8_t* h_s, const float* row_w,
                                            uint16_t* dh, uint16_t* act, float* dots, int num_cus, hipStream_t s);
 
+// The kernel such a product takes (op: MOE_GEMM_BF16_*; n_out and k_in as its
+// launch takes them): rows of its tiles, 16 in the few-rows kernel, and whether
+// neighbouring tiles start the contraction a step apart.
+struct GemmBf16Plan {
+    int tile_rows;
+    bool staggered;
+};
+GemmBf16Plan gemm_bf16_plan(int op, int El, int n_out, int k_in, int64_t rows_hint, int num_cus);
+
 hipError_t launch_silu_mul(const uint16_t* h, int64_t rows, int n, const int32_t* offsets, const int32_t* counts,
                            int El, uint16_t* act, int num_cus, hipStream_t s);
 hipError_t launch_silu_mul_bwd(const uint16_t* h, const uint16_t* dact, int64_t rows, int n, const int32_t* offsets,
