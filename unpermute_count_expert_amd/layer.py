@@ -123,8 +123,10 @@ class MoeTrainLayer:
     kernel, as are the down product's gradient and the activation's, which
     recomputes the activations; the router weights' gradient comes from the
     down product's gradient instead of its outputs.  8 bits round what the
-    gradients are taken at by up to 2^-4 of each value; the output is the same
-    with either checkpoint.
+    gradients are taken at by up to 2^-4 of each value, or 2^-10 of its
+    block's scale where that is more, so small values beside large ones among
+    32 become 0; magnitudes past 3.29e38 become infinite.  The output is the
+    same with either checkpoint.
 
     infer() is the forward pass alone: it keeps nothing.
 
