@@ -23,34 +23,15 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
     return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, false));   // lanes 2 3 0 1
 }
 
-typedef short v2s __attribute__((ext_vector_type(2)));
-
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float scale) {
-    uint2 c;
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        v2s p = {0, 0};
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, v[4 * i], v[4 * i + 1], scale, false);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, v[4 * i + 2], v[4 * i + 3], scale, true);
-        w[i] = __builtin_bit_cast(uint32_t, p);
-    }
-    c.x = w[0];
-    c.y = w[1];
-    return c;
+    return uint2{f32x4_to_e4m3_scaled(v[0], v[1], v[2], v[3], scale),
+                 f32x4_to_e4m3_scaled(v[4], v[5], v[6], v[7], scale)};
 }
 
 __device__ __forceinline__ uint4 decode8(uint2 c, float scale) {
-    const uint32_t w[2] = {c.x, c.y};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], scale, false);
-        const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], scale, true);
-        o[2 * i] = f32x2_to_bf16x2(lo[0], lo[1]);
-        o[2 * i + 1] = f32x2_to_bf16x2(hi[0], hi[1]);
-    }
-    return uint4{o[0], o[1], o[2], o[3]};
+    const f32x4 x = e4m3x4_to_f32_scaled(c.x, scale), y = e4m3x4_to_f32_scaled(c.y, scale);
+    return uint4{f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(y[0], y[1]),
+                 f32x2_to_bf16x2(y[2], y[3])};
 }
 
 // Rows are whole blocks, so the matrix is one line of them: a lane takes eight

@@ -256,9 +256,7 @@ __device__ __forceinline__ void unpack_pair(const v4u& v, v4f& x, v4f& y) {
 }
 
 // ---- the gated products' epilogues ----------------------------------------------
-typedef float v2f __attribute__((ext_vector_type(2)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
-typedef short v2s __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
@@ -279,17 +277,9 @@ __device__ __forceinline__ uint32_t over_lane_rows(uint32_t v, F f) {
     return f(b[0], b[1]);
 }
 
-// four fp32 over a power of two as e4m3 codes, and back
+// four fp32 over a power of two as e4m3 codes
 __device__ __forceinline__ uint32_t to_codes(const v4f& v, float scale) {
-    v2s c = {0, 0};
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[0], v[1], scale, false);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[2], v[3], scale, true);
-    return __builtin_bit_cast(uint32_t, c);
-}
-__device__ __forceinline__ v4f from_codes(uint32_t c, float scale) {
-    const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, false);
-    const v2f hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, true);
-    return v4f{lo[0], lo[1], hi[0], hi[1]};
+    return f32x4_to_e4m3_scaled(v[0], v[1], v[2], v[3], scale);
 }
 __device__ __forceinline__ uint32_t magnitude(const v4f& v) {
     uint32_t m = 0;
@@ -411,10 +401,10 @@ __device__ __forceinline__ float gated_bwd_rows(const Gate& gate, void* dh, int 
         } else {
             const auto gq = __builtin_amdgcn_permlane16_swap(in.h[p][0][0], in.h[p][0][1], false, false);
             const auto uq = __builtin_amdgcn_permlane16_swap(in.h[p][0][2], in.h[p][0][3], false, false);
-            gx = from_codes(gq[0], sc[0][p]);
-            gy = from_codes(gq[1], sc[0][p]);
-            ux = from_codes(uq[0], sc[1][p]);
-            uy = from_codes(uq[1], sc[1][p]);
+            gx = e4m3x4_to_f32_scaled(gq[0], sc[0][p]);
+            gy = e4m3x4_to_f32_scaled(gq[1], sc[0][p]);
+            ux = e4m3x4_to_f32_scaled(uq[0], sc[1][p]);
+            uy = e4m3x4_to_f32_scaled(uq[1], sc[1][p]);
         }
         dot += gated_bwd(gx, ux, d[2 * p], in.weight, act[0], dg[0], du[0]);
         dot += gated_bwd(gy, uy, d[2 * p + 1], in.weight, act[1], dg[1], du[1]);

@@ -137,6 +137,21 @@ __device__ __forceinline__ uint32_t e8m0_of(uint32_t m) {
 // (b = 0 is 2^-127 there, 255 makes a value or code NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b << 23); }
 
+// Four values over such a scale as e4m3 codes, and codes times their scale.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3_scaled(float a, float b, float c, float d, float scale) {
+    typedef short v2s __attribute__((ext_vector_type(2)));
+    v2s w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+    return __builtin_bit_cast(uint32_t, w);
+}
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 e4m3x4_to_f32_scaled(uint32_t codes, float scale) {
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, scale, false);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(codes, scale, true);
+    return f32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
 // eight bf16 values (one 16-byte load) as fp32
 __device__ __forceinline__ void bf16x8_to_f32(uint4 u, float (&v)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
