@@ -154,8 +154,9 @@ hipError_t launch_rows(const void* x, const uint8_t* scales, const int32_t* inv_
     by = by > topk ? topk : by;
     // Plain stores where the rows written fit the 256 MB behind the L2s, from
     // where the next product reads them, non-temporal ones past that.  2048
-    // columns, top-8, bf16 and restored rows, us: 4096 tokens plain 31 and 23,
-    // non-temporal 29 and 27; 16384 tokens 161 and 112, 106 and 105.
+    // columns, top-8, bf16 and restored rows, us, calls back to back: 4096 tokens
+    // plain 31 and 23, non-temporal 29 and 27; 16384 tokens 161 and 112, 106 and
+    // 105 (bf16 rows after the backward pass's other kernels 126).
     const bool nt = (int64_t)K * 2 * Mc * topk > (int64_t)256 << 20;
     auto* k = scales ? (nt ? k_rows<true, true> : k_rows<true, false>) : (nt ? k_rows<false, true> : k_rows<false, false>);
     k<<<dim3((unsigned)bx, (unsigned)by), kThreads, 0, s>>>(x, scales, inv_perm, topk_w, Mc, K, topk, out, out_rows,

@@ -77,10 +77,10 @@
 //    both and h needs no trip through memory.  It is kept for the backward
 //    pass as it is (KEEP): not at all, in bf16, or as e4m3 codes with a scale
 //    for 32 columns, which lie in one wave's four lane rows.
-//  * 16384 tokens, top-8, 128 experts, 768 x 2048, us: h not kept 726-748, bf16
-//    781-803, 8 bits 791-810, against 750 for the product and 95 for SiLU-mul.
-//    Backward from bf16 551, from 8 bits 540, against 395 for the product and
-//    163 for SiLU-mul's gradient, which leave out act and the dot products.
+//  * 16384 tokens, top-8, 128 experts, 768 x 2048, us: h not kept 726-760, bf16
+//    781-812, 8 bits 791-811, against 750 for the product and 95 for SiLU-mul.
+//    Backward from bf16 550-555, from 8 bits 540-548, against 395 for the product
+//    and 163 for SiLU-mul's gradient, which leave out act and the dot products.
 //  * The backward epilogue reads 2 or 4 and writes 6 bytes an element, half of
 //    the kernel's bytes, and costs 165 us: 70 for its operations (12 plain ones
 //    an element, an exponential and a reciprocal), the rest for memory.  With
@@ -1429,8 +1429,9 @@ GemmBf16Plan choose(int El, int n_out, int k_in, int64_t rows_hint, int num_cus)
             // Small tiles: work for every CU where the others leave some
             // idle, and more blocks to keep short walks' loads in flight; but
             // an expert's weights are read again for every 64 rows.  Over 400
-            // shapes the choice among the four is 2% slower than the best on
-            // average, over 20% in 1.6% of them and 50% at worst.
+            // shapes the choice among the four is 3% (forward) and 2% (backward)
+            // slower than the best on average, over 20% in 1.6% of the calls and
+            // 50% at worst.
             // 130 tokens over 64 experts of 672 x 2176, both ways, us: 114, with
             // small tiles 90; 8 experts, 309 rows each, 552 x 1408: 64 and 43;
             // 128 of 768 x 2048, forward, 64 rows each: 152, all small 175.
