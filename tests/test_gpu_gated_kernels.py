@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import unpermute_count_expert_amd as moe
+from tests import test_gpu_bf16_experts as base
 from tests import test_gpu_gated_experts as whole
 from tests.gpu_helpers import announce
 from tests.test_gpu_bf16_experts import (BF, DEV, F64, I32, TINY, bf, gen, i32, poison, segments, sentinel, valid_mask)
@@ -424,3 +425,80 @@ def test_each_kernel_past_32_bits(up, down):
     assert name(moe.moe_grouped_gemm_bf16_plan_info(moe.MOE_GEMM_BF16_SILU_MUL, *at, hint)) == up
     assert name(moe.moe_grouped_gemm_bf16_plan_info(moe.MOE_GEMM_BF16_DGRAD_SILU_MUL, 140, 4096, 2048, hint)) == down
     whole.test_gated_past_32_bits(hint)
+
+
+@pytest.mark.parametrize("kernel", KERNELS["backward"])
+def test_each_kernel_in_place_with_every_output(kernel):
+    """dh in h's place beside act, dots and router weights: the bits of the call that keeps h."""
+    n = N_OF["bf16"]
+    off, cap = segments(ROWS, 16)
+    mask = valid_mask(ROWS, off, cap)
+    g = gen(n + 3)
+    rows, w = bf((cap, K_ODD), g).to(DEV), bf((len(ROWS), K_ODD, n), g, K_ODD ** -0.5).to(DEV)
+    h, weights = bf((cap, 2 * n), g, 3.0).to(DEV), torch.rand(cap, generator=g).to(DEV)
+    hint, new = hint_of("backward", kernel, n, K_ODD), Guarded()
+    want, got = outputs("backward", "bf16", cap, n, new), outputs("backward", "bf16", cap, n, new)
+    call("backward", rows, w, i32(off), i32(ROWS), want, hint, (h, None), weights)
+    got[0].copy_(h)
+    call("backward", rows, w, i32(off), i32(ROWS), got, hint, (got[0], None), weights)
+    assert equal_rows(got, want, mask) and new.intact()
+    assert torch.equal(got[0][~mask.to(DEV)], h[~mask.to(DEV)])
+
+
+# ---- the layer ----------------------------------------------------------------------------
+@pytest.mark.parametrize("keep", [None, "bf16", "e4m3"])
+def test_layer_from_buffers_of_nan(keep):
+    """Every buffer that the layer takes starts as NaN (codes and scales as 255): the same bits."""
+    x, ids, tw, dout = base.batch(52, 37, topk=3)
+    want = base.explicit(whole.make_layer(51, keep, El=5), x, ids, tw, dout)
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)   # fills what torch.empty gives
+    try:
+        assert torch.isnan(torch.empty(5, device=DEV)).all()
+        layer = whole.make_layer(51, keep, El=5)
+        got = base.explicit(layer, x, ids, tw, dout)
+        alone = layer.infer(x, ids, tw)
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    if keep is not None:
+        assert torch.equal(alone, want[0])
+
+
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+def test_layer_without_rows_of_its_own(keep):
+    """Every token goes to experts elsewhere: zeros, and the weights' gradients stay."""
+    layer = whole.make_layer(53, keep, El=4)
+    x, ids, tw, dout = base.batch(54, 20)
+    ids = ids % 4   # the last four of eight are here
+    layer.grad_w13.fill_(2), layer.grad_w2.fill_(3)
+    out, saved = layer.forward(x, ids, tw)
+    for t in (out, *layer.backward(dout, saved), layer.infer(x, ids, tw)):
+        assert not t.any()
+    assert (layer.grad_w13 == 2).all() and (layer.grad_w2 == 3).all()
+
+
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+def test_layer_with_an_expert_picked_twice(keep):
+    """A token that picks one expert twice has two rows there, and pairs without an expert (-1) none: the output
+    against 64 bits, the gradients against their formulas at the kept values (six bf16 roundings, as in
+    test_layer_with_a_checkpoint)."""
+    layer = whole.make_layer(55, keep)
+    x, ids, tw, dout = base.batch(56, 60, topk=4)
+    ids[::2, 1] = ids[::2, 0]
+    ids[::3, 2] = ids[::3, 0]
+    ids[::5, 3] = -1
+    out, saved = layer.forward(x, ids, tw)
+    dx, dtw = layer.backward(dout, saved)
+    assert (dtw[::5, 3] == 0).all()
+    d = lambda t: t.cpu().double()
+    want = torch.zeros(x.shape, dtype=F64)
+    for t, picks in enumerate(ids.tolist()):
+        for j, e in enumerate(picks):
+            if e >= 0:
+                h = d(layer.w13[e]) @ d(x[t])
+                want[t] += d(tw[t, j]) * (d(layer.w2[e]) @ (silu(h[:layer.N]) * h[layer.N:]))
+    assert base.rel(out, want) <= 6 * 2.0 ** -8
+    for got, ref, what in zip((dx, dtw, layer.grad_w13, layer.grad_w2), whole.grads_at(layer, saved, tw, dout),
+                              ("dx", "dtw", "dw13", "dw2")):
+        assert base.rel(got, ref) <= 6 * 2.0 ** -8, (what, base.rel(got, ref))
